@@ -52,7 +52,7 @@ typedef enum {
   NLD_ERR_UNSUPPORTED = 8  /* shape outside what the kernels implement */
 } nld_status;
 
-enum { NLD_F32 = 0, NLD_BF16 = 1 };
+enum { NLD_F32 = 0, NLD_BF16 = 1, NLD_E4M3 = 2 /* KV caches only */ };
 
 /* Forward kinds accepted by nld_debug_logits. */
 enum { NLD_MODE_AR = 0, NLD_MODE_DRAFT = 1, NLD_MODE_VERIFY = 2, NLD_MODE_DIFFUSE = 3, NLD_MODE_QUAD = 4 };
@@ -443,6 +443,109 @@ nld_status nld_attention(const void* d_q, const void* d_kv_pool, const int32_t* 
                          int pages_per_seq, int n_pages, const int32_t* d_lens, int batch, int m,
                          int n_q_heads, int n_kv_heads, int head_dim, int block_size, int max_len,
                          void* d_out, void* cuda_stream);
+
+/*
+ * Head norm, rotation and cache write of a forward's new rows, in one pass (the step between the
+ * QKV projection and attention, for models with per-head norms of q and k, and for e4m3 caches).
+ * For row i of sequence b (token t = b*m + i), at cache slot s = lens[b] + i and position
+ * s + position_offset:
+ *   each head x of q and k:  y = x / sqrt(mean(x^2) + rms_eps) * gain   (if gains are given), then
+ *   rotate-half: o_j = y_j c_j - y_{j+hd/2} s_j,  o_{j+hd/2} = y_{j+hd/2} c_j + y_j s_j;
+ *   q goes to d_q_out, k and the unchanged v to slot s of the sequence's pages.
+ *   d_q, d_k, d_v    `dtype` (NLD_F32 or NLD_BF16) token rows of Hq*hd, Hkv*hd and Hkv*hd elements,
+ *                    q_ld / k_ld / v_ld elements apart (parts of one projection's output, say).
+ *   d_q_gain, d_k_gain  [hd] of `dtype`; both, or NULL for both: no norm.
+ *   d_rope           [rope_rows, hd/2] (cos, sin) fp32 pairs: row p holds the angles
+ *                    p * theta^(-2j/hd), j = 0..hd/2-1.
+ *   position_offset  position of cache slot 0 (the length of a shared prefix; else 0).
+ *   d_rows           [batch] or NULL: the first rows[b] of the m rows of sequence b are live, the
+ *                    others are padding: nothing of them is read or written.
+ *   d_q_out          [batch, m, Hq, hd] of `dtype`; may be d_q where q_ld = Hq*hd.
+ *   d_kv_pool        [n_pages][2][Hkv][64][hd] of `kv_dtype` (K then V per page).  NLD_F32 and
+ *                    NLD_BF16 rows are rounded once from fp32; NLD_E4M3 rows are e4m3(x / scale),
+ *                    round to nearest even, magnitudes over 448 (infinities too) saturated.
+ *   d_k_scale, d_v_scale  [Hkv] fp32 (> 0, finite) with NLD_E4M3, ignored otherwise.
+ *   d_page_table     [batch, pages_per_seq] int32 page ids (< n_pages); no two rows of a call may
+ *                    share a slot.
+ *   d_err            one int32 or NULL: a live row whose slot is outside its page table row, whose
+ *                    position is outside the rope table or whose page is outside the pool is left
+ *                    out, and NLD_DEVERR_KV_OVERFLOW is or-ed in.
+ * head_dim 64 or 128; pointers 16-byte aligned, q_ld, k_ld and v_ld multiples of 16 bytes.
+ * Stream-ordered on `cuda_stream`; returns after the launch.
+ */
+nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, long long k_ld, const void* d_v,
+                            long long v_ld, int dtype, const void* d_q_gain, const void* d_k_gain, float rms_eps,
+                            const float* d_rope, int rope_rows, int position_offset, const int32_t* d_lens,
+                            const int32_t* d_rows, int batch, int m, int n_q_heads, int n_kv_heads, int head_dim,
+                            void* d_q_out, void* d_kv_pool, int kv_dtype, const float* d_k_scale,
+                            const float* d_v_scale, const int32_t* d_page_table, int pages_per_seq, int n_pages,
+                            int32_t* d_err, void* cuda_stream);
+
+/*
+ * nld_attention over an e4m3 cache, as nld_qk_norm_rope writes it: K = k_scale[g] * k8,
+ * V = v_scale[g] * v8 for kv head g.  Half the bytes per key of the bf16 cache.
+ *   d_kv_pool    [n_pages][2][Hkv][64][128] e4m3.  Slots that no query of a sequence sees may hold
+ *                anything (NaN patterns too).
+ *   d_k_scale, d_v_scale  [Hkv] fp32.
+ *   d_err        one int32 or NULL: a lens[b] outside 0..pages_per_seq*64-m is clamped, a page id
+ *                outside the pool reads as zeros, and NLD_DEVERR_KV_OVERFLOW is or-ed in.
+ * The other arguments, the mask and the conventions are those of nld_attention (d_q and d_out
+ * bf16, 16-byte aligned).  Scores, maxima and sums are fp32; the probabilities are rounded to fp16 for
+ * their product with V.
+ */
+nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float* d_k_scale, const float* d_v_scale,
+                            const int32_t* d_page_table, int pages_per_seq, int n_pages, const int32_t* d_lens,
+                            int batch, int m, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
+                            int max_len, void* d_out, int32_t* d_err, void* cuda_stream);
+
+/*
+ * nld_attention for a batch whose sequences all start with the same shared_len keys (a system
+ * prompt, a document), stored once: every query sees those keys, then the keys of its own sequence
+ * under the block-causal mask.  The prefix's keys are read once for the rows of the whole batch.
+ *   d_shared_pages  [n_shared_pages] int32 page ids of the prefix, n_shared_pages*64 >= shared_len;
+ *                   shared_len 0 (the pointer may then be NULL) is nld_attention.
+ *   d_page_table, d_lens, max_len  a sequence's own pages and keys, as in nld_attention, counted
+ *                   from the end of the prefix: its slot 0 holds position shared_len (the
+ *                   position_offset of nld_qk_norm_rope).
+ *   d_workspace     16-byte aligned, nld_attention_shared_workspace_size() bytes: the prefix's fp32
+ *                   partial of every (row, query head).  Calls sharing it must not overlap.
+ *   d_err           one int32 or NULL: a lens[b] outside 0..pages_per_seq*64-m is clamped and
+ *                   NLD_DEVERR_KV_OVERFLOW is or-ed in; NLD_DEVERR_TIMEOUT if a bounded wait ran out.
+ * Slots behind a sequence's last key, and behind the prefix's, may hold anything.
+ * Two launches on `cuda_stream`; returns after them.
+ */
+size_t nld_attention_shared_workspace_size(int batch, int m, int n_q_heads);
+nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const int32_t* d_shared_pages,
+                                int n_shared_pages, int shared_len, const int32_t* d_page_table,
+                                int pages_per_seq, int n_pages, const int32_t* d_lens, int batch, int m,
+                                int n_q_heads, int n_kv_heads, int head_dim, int block_size, int max_len,
+                                void* d_out, void* d_workspace, size_t workspace_bytes, int32_t* d_err,
+                                void* cuda_stream);
+
+/*
+ * The next token of each row of logits, sampled with a given uniform number (the stochastic
+ * counterpart of nld_lm_head_argmax).  With w_i = exp((x_i - max x) / T), and the tokens in the
+ * order of falling logits, equal logits by index:
+ *   top-k keeps the first k tokens;
+ *   top-p keeps those of these before which less than p of their mass lies (at least one);
+ *   min-p keeps those of these with w_i >= min_p (at least the likeliest);
+ *   the token is the first kept one, by index, up to and with which more than u of the kept mass
+ *   lies; its probability is its share of that mass.
+ *   d_logits       [rows] rows of `vocab` elements of `dtype` (NLD_F32 or NLD_BF16), `ld` apart.
+ *                  -inf and NaN are never sampled; if one is +inf, so are all of that value alone.
+ *   d_u            [rows] in [0, 1); other values are clamped to it (NaN to 0).
+ *   d_temperature  [rows] or NULL (1): not over 0, or NaN: the largest logit, lowest index, with
+ *                  probability 1.
+ *   d_top_k [rows] int32, d_top_p, d_min_p [rows] fp32, or NULL.  Off: k <= 0, p >= 1 or NaN,
+ *                  min_p <= 0 or NaN.
+ *   d_tokens_out   [rows] int32; -1, with probability 0, for a row without a finite or +inf logit.
+ *   d_prob_out     [rows] fp32 or NULL.
+ * Weights are held to 2^-44 of the largest and summed exactly, so repeated calls give the same
+ * tokens.  1 <= vocab <= 2^19.  Stream-ordered on `cuda_stream`; returns after the launch.
+ */
+nld_status nld_sample(const void* d_logits, int dtype, long long ld, int rows, int vocab, const float* d_u,
+                      const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
+                      const float* d_min_p, int32_t* d_tokens_out, float* d_prob_out, void* cuda_stream);
 
 #ifdef __cplusplus
 }

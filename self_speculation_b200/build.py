@@ -13,7 +13,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libnld.so")
-SOURCES = ["nld_api.cu", "gemm_tc.cu", "gemm_simt.cu", "attention.cu", "decode_kernels.cu"]
+SOURCES = ["nld_api.cu", "gemm_tc.cu", "gemm_simt.cu", "attention.cu", "decode_kernels.cu",
+           "attention_q8.cu", "qkv_write.cu", "sampling.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -33,7 +34,7 @@ def _stale() -> bool:
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
     if not force and not _stale():
         return LIB
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--shared", "-Xcompiler", "-fPIC", "--threads", "0",
            "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", LIB + ".tmp"]
     if ptxas_v:
         cmd += ["-Xptxas", "-v"]

@@ -2181,4 +2181,219 @@ nld_status nld_attention(const void* d_q, const void* d_kv_pool, const int32_t* 
   return NLD_OK;
 }
 
+// ------------------------------------------------- operators around the paged cache --
+
+static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, long long k_ld, const void* d_v,
+                            long long v_ld, int dtype, const void* d_q_gain, const void* d_k_gain, float rms_eps,
+                            const float* d_rope, int rope_rows, int position_offset, const int32_t* d_lens,
+                            const int32_t* d_rows, int batch, int m, int n_q_heads, int n_kv_heads, int head_dim,
+                            void* d_q_out, void* d_kv_pool, int kv_dtype, const float* d_k_scale,
+                            const float* d_v_scale, const int32_t* d_page_table, int pages_per_seq, int n_pages,
+                            int32_t* d_err, void* cuda_stream) {
+  if (!d_q || !d_k || !d_v || !d_rope || !d_lens || !d_q_out || !d_kv_pool || !d_page_table)
+    return fail(nullptr, NLD_ERR_ARG, "NULL pointer argument");
+  if (dtype != NLD_F32 && dtype != NLD_BF16) return fail(nullptr, NLD_ERR_ARG, "dtype must be NLD_F32 or NLD_BF16");
+  if (kv_dtype != NLD_F32 && kv_dtype != NLD_BF16 && kv_dtype != NLD_E4M3)
+    return fail(nullptr, NLD_ERR_ARG, "kv_dtype must be NLD_F32, NLD_BF16 or NLD_E4M3");
+  if (!d_q_gain != !d_k_gain) return fail(nullptr, NLD_ERR_ARG, "q and k gains: both or neither");
+  if (kv_dtype == NLD_E4M3 && (!d_k_scale || !d_v_scale))
+    return fail(nullptr, NLD_ERR_ARG, "an e4m3 cache needs k and v scales");
+  if (head_dim != 64 && head_dim != 128) return fail(nullptr, NLD_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (batch < 1 || m < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads > 65536 || n_kv_heads > 65536)
+    return fail(nullptr, NLD_ERR_ARG, "bad batch/m/head counts");
+  if (!(rms_eps >= 0.f)) return fail(nullptr, NLD_ERR_ARG, "rms_eps must be >= 0");
+  if (rope_rows < 1 || position_offset < 0) return fail(nullptr, NLD_ERR_ARG, "bad rope_rows or position_offset");
+  if (pages_per_seq < 1 || pages_per_seq > INT32_MAX / kPage || n_pages < 1)
+    return fail(nullptr, NLD_ERR_ARG, "bad page table or pool size");
+  const int per16 = dtype == NLD_F32 ? 4 : 8;
+  if (q_ld < static_cast<long long>(n_q_heads) * head_dim || k_ld < static_cast<long long>(n_kv_heads) * head_dim ||
+      v_ld < static_cast<long long>(n_kv_heads) * head_dim || q_ld % per16 || k_ld % per16 || v_ld % per16)
+    return fail(nullptr, NLD_ERR_ARG, "row distances must hold a row and be multiples of 16 bytes");
+  if (!aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) || !aligned16(d_q_out) || !aligned16(d_kv_pool) ||
+      !aligned16(d_rope) || !aligned16(d_q_gain) || !aligned16(d_k_gain))
+    return fail(nullptr, NLD_ERR_ARG, "pointers must be 16-byte aligned");
+  // one thread per 16 bytes of half a head at most; the grid's x extent bounds them
+  if (static_cast<double>(batch) * m * (n_q_heads + 2.0 * n_kv_heads) * 16 > 2147483647.0 * 256)
+    return fail(nullptr, NLD_ERR_ARG, "batch * m too large");
+  QkvWriteArgs a{};
+  a.q = d_q;
+  a.k = d_k;
+  a.v = d_v;
+  a.q_ld = q_ld;
+  a.k_ld = k_ld;
+  a.v_ld = v_ld;
+  a.q_gain = d_q_gain;
+  a.k_gain = d_k_gain;
+  a.eps = rms_eps;
+  a.rope = reinterpret_cast<const float2*>(d_rope);
+  a.rope_rows = rope_rows;
+  a.position_offset = position_offset;
+  a.lens = d_lens;
+  a.rows = d_rows;
+  a.batch = batch;
+  a.m = m;
+  a.Hq = n_q_heads;
+  a.Hkv = n_kv_heads;
+  a.hd = head_dim;
+  a.q_out = d_q_out;
+  a.pool = d_kv_pool;
+  a.k_scale = d_k_scale;
+  a.v_scale = d_v_scale;
+  a.page_table = d_page_table;
+  a.pps = pages_per_seq;
+  a.n_pages = n_pages;
+  a.err = d_err;
+  const cudaError_t e = launch_qkv_write(static_cast<cudaStream_t>(cuda_stream), a, dtype, kv_dtype, device_sms());
+  if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "cache write launch failed: %s", cudaGetErrorString(e));
+  return NLD_OK;
+}
+
+// Argument checks common to the attention operators below.
+static nld_status attn_check(const void* d_q, const void* d_kv_pool, const int32_t* d_page_table, int pages_per_seq,
+                             int n_pages, const int32_t* d_lens, int batch, int m, int n_q_heads, int n_kv_heads,
+                             int head_dim, int block_size, int max_len, const void* d_out) {
+  if (!d_q || !d_kv_pool || !d_page_table || !d_lens || !d_out)
+    return fail(nullptr, NLD_ERR_ARG, "NULL pointer argument");
+  if (batch < 1 || m < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads)
+    return fail(nullptr, NLD_ERR_ARG, "bad batch/m/head counts");
+  if (head_dim != 128) return fail(nullptr, NLD_ERR_UNSUPPORTED, "head_dim must be 128");
+  if (block_size < 1) return fail(nullptr, NLD_ERR_ARG, "block_size must be >= 1");
+  if (pages_per_seq < 1 || pages_per_seq > INT32_MAX / kPage || max_len < m || max_len > pages_per_seq * kPage)
+    return fail(nullptr, NLD_ERR_ARG, "max_len outside m..pages_per_seq*64");
+  if (n_pages < 1 || static_cast<long long>(n_pages) * 2 * n_kv_heads * kPage > INT32_MAX)
+    return fail(nullptr, NLD_ERR_ARG, "bad pool size");
+  if (static_cast<long long>(batch) * m * n_q_heads > INT32_MAX / 2 || n_kv_heads > 65535)
+    return fail(nullptr, NLD_ERR_ARG, "batch * m * heads too large");
+  if (!aligned16(d_q) || !aligned16(d_kv_pool) || !aligned16(d_out))
+    return fail(nullptr, NLD_ERR_ARG, "q, the pool and out must be 16-byte aligned");
+  return NLD_OK;
+}
+
+nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float* d_k_scale, const float* d_v_scale,
+                            const int32_t* d_page_table, int pages_per_seq, int n_pages, const int32_t* d_lens,
+                            int batch, int m, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
+                            int max_len, void* d_out, int32_t* d_err, void* cuda_stream) {
+  TRY(attn_check(d_q, d_kv_pool, d_page_table, pages_per_seq, n_pages, d_lens, batch, m, n_q_heads, n_kv_heads,
+                 head_dim, block_size, max_len, d_out));
+  if (!d_k_scale || !d_v_scale) return fail(nullptr, NLD_ERR_ARG, "NULL scale pointer");
+  AttnQ8Args a{};
+  a.m = m;
+  a.Hq = n_q_heads;
+  a.Hkv = n_kv_heads;
+  a.G = n_q_heads / n_kv_heads;
+  int mt = 1;
+  attn_q8_plan(batch, max_len, device_sms(), a, &mt);
+  if (static_cast<long long>(batch) * a.r_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
+  a.q = d_q;
+  a.out = d_out;
+  a.pool = d_kv_pool;
+  a.k_scale = d_k_scale;
+  a.v_scale = d_v_scale;
+  a.lens = d_lens;
+  a.page_table = d_page_table;
+  a.pps = pages_per_seq;
+  a.n_pages = n_pages;
+  a.block_size = block_size;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
+  a.err = d_err;
+  const cudaError_t e = launch_attention_q8(static_cast<cudaStream_t>(cuda_stream), a, batch, mt);
+  if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
+  return NLD_OK;
+}
+
+size_t nld_attention_shared_workspace_size(int batch, int m, int n_q_heads) {
+  if (batch < 1 || m < 1 || n_q_heads < 1) return 0;
+  return static_cast<size_t>(batch) * m * n_q_heads * (128 + 2) * sizeof(float);
+}
+
+nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const int32_t* d_shared_pages,
+                                int n_shared_pages, int shared_len, const int32_t* d_page_table,
+                                int pages_per_seq, int n_pages, const int32_t* d_lens, int batch, int m,
+                                int n_q_heads, int n_kv_heads, int head_dim, int block_size, int max_len,
+                                void* d_out, void* d_workspace, size_t workspace_bytes, int32_t* d_err,
+                                void* cuda_stream) {
+  TRY(attn_check(d_q, d_kv_pool, d_page_table, pages_per_seq, n_pages, d_lens, batch, m, n_q_heads, n_kv_heads,
+                 head_dim, block_size, max_len, d_out));
+  if (shared_len < 0 || (shared_len > 0 && (!d_shared_pages || (shared_len - 1) / kPage >= n_shared_pages)))
+    return fail(nullptr, NLD_ERR_ARG, "shared_len outside 0..n_shared_pages*64");
+  const size_t need = nld_attention_shared_workspace_size(batch, m, n_q_heads);
+  if (shared_len > 0 && (!d_workspace || workspace_bytes < need || !aligned16(d_workspace)))
+    return fail(nullptr, NLD_ERR_ARG, "workspace must be 16-byte aligned and at least %zu bytes", need);
+  const cudaError_t ae = init_shared_attention_attributes();
+  if (ae != cudaSuccess) {
+    cudaGetLastError();
+    return fail(nullptr, NLD_ERR_CUDA, "setting kernel shared-memory limits failed: %s", cudaGetErrorString(ae));
+  }
+  CUtensorMap map;
+  if (!make_map_bf16(&map, d_kv_pool, 128, static_cast<uint64_t>(n_pages) * 2 * n_kv_heads * kPage, kPage))
+    return fail(nullptr, NLD_ERR_CUDA, "tensor map encode failed (pool)");
+  const int sms = device_sms();
+  const AttnCapacity cap = [](int S, int NW, int stages, int tc) { return attn_device_capacity(false, S, NW, stages, tc); };
+  AttnArgs a{};
+  a.q = d_q;
+  a.out = d_out;
+  a.out_ld = static_cast<size_t>(n_q_heads) * 128;
+  a.Hq = n_q_heads;
+  a.Hkv = n_kv_heads;
+  a.hd = 128;
+  a.block_size = block_size;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
+  a.err = d_err;
+  if (shared_len > 0) {
+    a.part_o = static_cast<float*>(d_workspace);   // rows of 512 bytes, then the (max, sum) pairs
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(batch) * m * n_q_heads * 128);
+  }
+  AttnArgs own = a, pre = a;
+  own.share = kOwnPass;
+  own.m = m;
+  own.lens = d_lens;
+  own.page_table = d_page_table;
+  own.pps = pages_per_seq;
+  attn_plan(batch, m, n_q_heads, n_kv_heads, max_len, sms, own, cap, 0, 0, g_attn_kernel.load(), g_attn_tile.load(), false);
+  pre.share = kPrefixPass;
+  pre.m = batch * m;
+  pre.key_end = shared_len;
+  pre.page_table = d_shared_pages;
+  pre.pps = (shared_len + kPage - 1) / kPage;
+  attn_plan(1, pre.m, n_q_heads, n_kv_heads, std::max(1, shared_len), sms, pre, cap, 0, 0, g_attn_kernel.load(),
+            g_attn_tile.load(), false);
+  if (static_cast<long long>(batch) * own.q_tiles > 65535 || pre.q_tiles > 65535)
+    return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
+  cudaError_t e = cudaSuccess;
+  if (shared_len > 0) e = launch_attention_mma(static_cast<cudaStream_t>(cuda_stream), &map, pre, 1, false);
+  // the own pass may start beside the prefix pass: it waits for it before its merge
+  if (e == cudaSuccess)
+    e = launch_attention_mma(static_cast<cudaStream_t>(cuda_stream), &map, own, batch, shared_len > 0);
+  if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
+  return NLD_OK;
+}
+
+nld_status nld_sample(const void* d_logits, int dtype, long long ld, int rows, int vocab, const float* d_u,
+                      const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
+                      const float* d_min_p, int32_t* d_tokens_out, float* d_prob_out, void* cuda_stream) {
+  if (!d_logits || !d_u || !d_tokens_out) return fail(nullptr, NLD_ERR_ARG, "NULL pointer argument");
+  if (dtype != NLD_F32 && dtype != NLD_BF16) return fail(nullptr, NLD_ERR_ARG, "dtype must be NLD_F32 or NLD_BF16");
+  if (rows < 1 || vocab < 1 || vocab > (1 << 19)) return fail(nullptr, NLD_ERR_ARG, "rows >= 1 and vocab in 1..2^19 required");
+  if (ld < vocab) return fail(nullptr, NLD_ERR_ARG, "ld must be at least vocab");
+  if (reinterpret_cast<uintptr_t>(d_logits) % (dtype == NLD_F32 ? 4 : 2))
+    return fail(nullptr, NLD_ERR_ARG, "logits must be aligned to their type");
+  SampleArgs a{};
+  a.logits = d_logits;
+  a.ld = ld;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.u = d_u;
+  a.temperature = d_temperature;
+  a.top_k = d_top_k;
+  a.top_p = d_top_p;
+  a.min_p = d_min_p;
+  a.tokens = d_tokens_out;
+  a.prob = d_prob_out;
+  const cudaError_t e = launch_sample(static_cast<cudaStream_t>(cuda_stream), a, dtype);
+  if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "sampling launch failed: %s", cudaGetErrorString(e));
+  return NLD_OK;
+}
+
 }  // extern "C"

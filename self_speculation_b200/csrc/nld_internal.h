@@ -139,6 +139,9 @@ struct alignas(64) ChainArgs {
   WarmPhase next[2];
 };
 
+// The two launches of the shared-prefix attention (AttnArgs::share; 0: the plain attention).
+constexpr int kOwnPass = 1, kPrefixPass = 2;
+
 struct AttnArgs {
   const void* q;        // [M, Hq, hd]
   void* out;            // [M, Hq, hd] rows out_ld elements apart (tensor-core path)
@@ -165,6 +168,60 @@ struct AttnArgs {
                         // causal; pre-draft row k+1+a*k+j sees the prefix, rows 0..a and its block
   unsigned long long* trace;   // optional per-CTA timestamps (profiling hook), or null
   int* err;
+  // shared-prefix attention
+  int share;            // 0, kOwnPass or kPrefixPass
+  int key_end;          // prefix pass: keys of the prefix
+  float* part_o;        // [tokens x Hq][128] unnormalised prefix O (own pass: null = no prefix)
+  float2* part_ml;      // [tokens x Hq] its running max (log2 units) and sum
+};
+
+// Head norm, rotation and cache write of the rows of a forward (nld_qk_norm_rope).
+struct QkvWriteArgs {
+  const void *q, *k, *v;        // token rows q_ld / k_ld / v_ld elements apart
+  long long q_ld, k_ld, v_ld;
+  const void *q_gain, *k_gain;  // [hd], both or neither
+  float eps;
+  const float2* rope;           // [rope_rows][hd / 2] (cos, sin)
+  int rope_rows, position_offset;
+  const int* lens;              // [batch]
+  const int* rows;              // [batch] live rows, or null
+  int batch, m, Hq, Hkv, hd;
+  void* q_out;                  // [batch, m, Hq, hd]
+  void* pool;                   // [n_pages][2][Hkv][64][hd]
+  const float *k_scale, *v_scale;   // [Hkv] (e4m3)
+  const int* page_table;
+  int pps, n_pages;
+  int groups;                   // head groups of a token (set by the launcher)
+  int* err;
+};
+
+// Attention over the e4m3 cache (nld_attention_q8).
+struct AttnQ8Args {
+  const void* q;                // [batch, m, Hq, 128] bf16
+  void* out;
+  const void* pool;             // [n_pages][2][Hkv][64][128] e4m3
+  const float *k_scale, *v_scale;   // [Hkv]
+  const int* lens;
+  const int* page_table;
+  int pps, n_pages;
+  int m, Hq, Hkv, G, block_size;
+  int r_tiles, S;               // tiles of query rows, KV splits (cluster size)
+  float scale_log2;             // log2(e) / sqrt(hd)
+  int* err;
+};
+
+// Token sampling (nld_sample).
+struct SampleArgs {
+  const void* logits;           // rows ld elements apart
+  long long ld;
+  int rows, vocab;
+  const float* u;
+  const float* temperature;     // [rows] or null (1)
+  const int* top_k;             // [rows] or null (off)
+  const float* top_p;
+  const float* min_p;
+  int* tokens;
+  float* prob;                  // [rows] or null
 };
 
 // ---- host-side launchers (each returns cudaError_t of the launch) -----------------------
@@ -179,6 +236,12 @@ cudaError_t launch_attention_mma(cudaStream_t st, const CUtensorMap* tmKV, const
                                  int batch, bool pdl);
 cudaError_t launch_attention_simt(cudaStream_t st, const AttnArgs& a, int batch, bool f32,
                                   int max_kv, bool pdl);
+
+cudaError_t init_shared_attention_attributes();
+cudaError_t launch_qkv_write(cudaStream_t st, QkvWriteArgs a, int dtype, int kv_dtype, int sms);
+void attn_q8_plan(int batch, int max_len, int sms, AttnQ8Args& a, int* mt);
+cudaError_t launch_attention_q8(cudaStream_t st, const AttnQ8Args& a, int batch, int mt);
+cudaError_t launch_sample(cudaStream_t st, const SampleArgs& a, int dtype);
 
 struct EmbedArgs {
   const void* E;        // [V+1, d]
