@@ -1318,13 +1318,15 @@ cudaError_t init_kernel_attributes() {
   return cudaSuccess;
 }
 
-// The same for the two passes of the shared-prefix attention, once per device.
+// The same for the two passes of the shared-prefix attention, once per device; the plain kernels' too:
+// the split planner asks for their occupancy, which without the opt-in is none.
 cudaError_t init_shared_attention_attributes() {
   static std::atomic<bool> done[64];
   int dev = 0, optin = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  if ((e = init_kernel_attributes()) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
   for (int share : {kPrefixPass, kOwnPass})
     for (int v = 0; v < 6; ++v) {
