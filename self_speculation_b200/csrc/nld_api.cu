@@ -2376,6 +2376,7 @@ nld_status nld_sample(const void* d_logits, int dtype, long long ld, int rows, i
   if (!d_logits || !d_u || !d_tokens_out) return fail(nullptr, NLD_ERR_ARG, "NULL pointer argument");
   if (dtype != NLD_F32 && dtype != NLD_BF16) return fail(nullptr, NLD_ERR_ARG, "dtype must be NLD_F32 or NLD_BF16");
   if (rows < 1 || vocab < 1 || vocab > (1 << 19)) return fail(nullptr, NLD_ERR_ARG, "rows >= 1 and vocab in 1..2^19 required");
+  if (rows > INT32_MAX / 8) return fail(nullptr, NLD_ERR_ARG, "too many rows");   // 8 CTAs of a row at most
   if (ld < vocab) return fail(nullptr, NLD_ERR_ARG, "ld must be at least vocab");
   if (reinterpret_cast<uintptr_t>(d_logits) % (dtype == NLD_F32 ? 4 : 2))
     return fail(nullptr, NLD_ERR_ARG, "logits must be aligned to their type");
@@ -2391,7 +2392,7 @@ nld_status nld_sample(const void* d_logits, int dtype, long long ld, int rows, i
   a.min_p = d_min_p;
   a.tokens = d_tokens_out;
   a.prob = d_prob_out;
-  const cudaError_t e = launch_sample(static_cast<cudaStream_t>(cuda_stream), a, dtype);
+  const cudaError_t e = launch_sample(static_cast<cudaStream_t>(cuda_stream), a, dtype, device_sms());
   if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "sampling launch failed: %s", cudaGetErrorString(e));
   return NLD_OK;
 }

@@ -222,6 +222,7 @@ struct SampleArgs {
   const float* min_p;
   int* tokens;
   float* prob;                  // [rows] or null
+  int S, part;                  // CTAs of a row, 16-byte vectors of a warp's part of a slice (set by the launcher)
 };
 
 // ---- host-side launchers (each returns cudaError_t of the launch) -----------------------
@@ -241,7 +242,7 @@ cudaError_t init_shared_attention_attributes();
 cudaError_t launch_qkv_write(cudaStream_t st, QkvWriteArgs a, int dtype, int kv_dtype, int sms);
 void attn_q8_plan(int batch, int max_len, int sms, AttnQ8Args& a, int* mt);
 cudaError_t launch_attention_q8(cudaStream_t st, const AttnQ8Args& a, int batch, int mt);
-cudaError_t launch_sample(cudaStream_t st, const SampleArgs& a, int dtype);
+cudaError_t launch_sample(cudaStream_t st, const SampleArgs& a, int dtype, int sms);
 
 struct EmbedArgs {
   const void* E;        // [V+1, d]

@@ -124,6 +124,32 @@ def test_whole_vocabularies(dtype, vocab):
           [0.0, 0.0, 0.0, 0.0, 0.0, 0.01])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_largest_vocabulary(dtype):
+    # fp32: slices over the shared memory
+    x = logits(3, 1 << 19, dtype, seed=8)
+    check(x, us(3), [1.0, 0.8, 1.2], [0, 3000, 0], [1.0, 0.9, 0.97], [0.001, 0.0, 0.0])
+
+
+@pytest.mark.parametrize("dtype,vocab", [("f32", 8191), ("f32", 16385), ("bf16", 40000), ("f32", 70001)])
+def test_rows_at_every_alignment(dtype, vocab):
+    # views into one row of numbers, each an element further on
+    flat = logits(1, vocab + 9, dtype, seed=9)[0].cuda()
+    for off in range(9):
+        x = flat[off:off + vocab][None]
+        check(x, us(1, seed=off), 1.1, 40 if off % 2 else None, 0.95)
+
+
+def test_flat_and_narrow_distributions():
+    # a whole vocabulary in one bin of the first search, and logits around zero
+    g = torch.Generator().manual_seed(3)
+    x = torch.rand(4, 50000, generator=g) * 1e-3
+    x[1] = torch.randn(50000, generator=g) * 1e-30
+    x[2] = 7.0 + torch.randint(0, 40, (50000,), generator=g) * 2.0 ** -20
+    check(x, us(4), 1.0, [30000, 0, 20000, 0], [0.4, 0.7, 1.0, 0.31])
+    check(x, us(4), [1e-4, 1e-31, 1e-6, 1e30], [0, 500, 0, 100], [0.8, 1.0, 0.5, 0.5], 0.1)
+
+
 def test_strided_rows_side_stream_graph_and_no_prob():
     import self_speculation_b200 as nb
     big = logits(5, 4000, seed=7).cuda()
