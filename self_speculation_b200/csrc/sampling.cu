@@ -15,7 +15,9 @@
 // halving of the weight; the next over the order-preserving keys inside the border's bin, until
 // that bin is one key (three levels for fp32, two for bf16, whatever the values).  Every
 // CTA counts its slice; one cluster barrier later each of them finds the bin from all CTAs'
-// range sums and that range's bins over distributed shared memory.
+// range sums and that range's bins over distributed shared memory.  Where the first histogram leaves
+// at most kList tokens (most calls with top-k, and peaked rows), one CTA ranks them against one
+// another instead, and neither further levels nor another pass over the row follow.
 //
 // Masses are sums of 64-bit fixed-point weights (2^44 at the row's largest logit; up to 2^19
 // tokens fit): their sums do not depend on the order of addition, so neither do the borders or the
@@ -36,19 +38,23 @@ constexpr int kMaxS = 8;            // CTAs of a row
 constexpr int kBins = 1024;
 constexpr int kRanges = 32;         // of 32 bins
 constexpr float kPerOctave = 20.f;  // bins per halving: the last one starts at 2^-51, no weight
+constexpr int kList = kThreads / 2;   // tokens ranked against one another
+constexpr float kFltMax = 3.402823466e38f;
 constexpr double kOne = 17592186044416.0;   // 2^44: the weight of the largest logit
 
 typedef unsigned long long u64;
 
-// Keys in the order of the values, of as many bits as the type has; -inf has the key kInf.
+// Keys in the order of the values, of as many bits as the type has; -inf has the key kInf.  (A NaN's key
+// is over that of +inf or under that of -inf.)
 template <typename T>
 struct Key;
 template <>
 struct Key<float> {
   static constexpr int n = 4;   // logits per 16 bytes
+  typedef uint4 Quad;           // 4 logits
   static constexpr uint32_t kInf = 0x007fffffu;
   static NLD_DEV uint32_t of(float x) {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x + 0.f);   // -0 as +0
     return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
   }
   static NLD_DEV float value(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
@@ -58,84 +64,109 @@ struct Key<float> {
     x[2] = __uint_as_float(v.z);
     x[3] = __uint_as_float(v.w);
   }
-  static NLD_DEV uint4 pack(const float (&x)[4]) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  static NLD_DEV float most(const uint4& v) {   // the largest; NaN does not count
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
 };
 template <>
 struct Key<__nv_bfloat16> {
   static constexpr int n = 8;
+  typedef uint2 Quad;
   static constexpr uint32_t kInf = 0x007fu;
   static NLD_DEV uint32_t of(float x) { return Key<float>::of(x) >> 16; }
   static NLD_DEV float value(uint32_t k) {
     return __uint_as_float((k & 0x8000u) ? (k ^ 0x8000u) << 16 : (k ^ 0xffffu) << 16);
   }
-  static NLD_DEV void unpack(const uint4& v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  static NLD_DEV void unpack(const uint2& v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x << 16);
+    x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16);
+    x[3] = __uint_as_float(v.y & 0xffff0000u);
   }
-  static NLD_DEV uint4 pack(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = (__float_as_uint(x[2 * i]) >> 16) | (__float_as_uint(x[2 * i + 1]) & 0xffff0000u);
-    return make_uint4(w[0], w[1], w[2], w[3]);
+  static NLD_DEV float most(const uint4& v) {
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const __nv_bfloat162 m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+    return fmaxf(__low2float(m), __high2float(m));
   }
 };
-// NaN counts as -inf, -0 as +0 (equal values must have equal keys).
-NLD_DEV float plain_logit(float v) { return (v == v) ? v + 0.f : -INFINITY; }
+
+// For Weigh::biased: 1.5 2^52, the polynomial from its highest coefficient on, 2^52.  (In constant memory, an
+// operand that costs no instruction: as literals they were two moves each.)
+__constant__ double kExp[8] = {6755399441055744.0,     1.2716085030349987e-09, 1.4676444621898709e-07, 1.355080777749983e-05,
+                               0.000938384792486206, 0.043321698784996608,   1.0,                    4503599627370496.0};
+
+__device__ const double kTab[16] = {17592186044416.0, 18371058661769.06, 19184414915921.48, 20033781527906.22,
+                                    20920752812471.082, 21846993670708.133, 22814242715178.152, 23824315533396.16,
+                                    24879108095803.8, 25980600314625.527, 27130859760288.855, 28332045542384.562,
+                                    29586412362451.676, 30896314746194.61, 32264211463076.527, 33692670141584.85};   // 2^(44 + j / 16)
 
 // Weights of a row's logits.
 struct Weigh {
-  float top, half_top;
-  float steps, more;  // their product: bins of the first level per unit of (max x - x) / 2
+  float top, half_top;   // the largest logit; FLT_MAX for +inf (then `low` leaves only those of +inf)
+  float low;             // logits under it have no weight (NaN compares as one of them)
+  float steps, more;     // their product: bins of the first level per unit of (max x - x) / 2
   double top_d, inv_t, s16;
-  const double* tab;  // 2^(j / 16), j = 0..15
+  const double* tab;     // 2^(44 + j / 16), j = 0..15, j 2^16 off the high words (k's low bits add it back)
   NLD_DEV void init(float top_, float temperature, const double* tab_) {
-    top = top_;
-    half_top = 0.5f * top_;   // halves: the difference of two finite logits may exceed fp32
-    top_d = static_cast<double>(top_);
+    top = fminf(top_, kFltMax);
+    half_top = 0.5f * top;   // halves: the difference of two finite logits may exceed fp32
+    top_d = static_cast<double>(top);
     inv_t = 1.0 / static_cast<double>(temperature);
     s16 = inv_t * 23.083120654223414;   // 16 log2(e)
+    // 50 halvings down (fp32 rounding leaves it under 120); 2^-45 rounds to nothing
+    low = top_ > kFltMax ? top_ : fmaxf(static_cast<float>(top_d - 34.657 * static_cast<double>(temperature)), -kFltMax);
     const double per = inv_t * (2.0 * 1.4426950408889634 * kPerOctave);
     steps = static_cast<float>(fmin(per, 1e38));
-    more = per > 1e38 ? static_cast<float>(per / 1e38) : 1.f;
+    more = per > 1e38 ? static_cast<float>(per * 1e-38) : 1.f;
     tab = tab_;
   }
-  // Bin of the first level: whole, not falling as x falls; kBins - 1: no weight (-inf, and all but the
-  // largest where that is +inf).
+  // Bin of the first level of a logit not under `low`: not falling as x falls.
   NLD_DEV int bin(float x) const {
-    if (x == top) return 0;
-    const float d = (half_top - 0.5f * x) * steps * more;
-    return d < static_cast<float>(kBins - 1) ? static_cast<int>(d) : kBins - 1;   // (inf, and 0 x inf = NaN: the last)
+    float d = (half_top - 0.5f * fminf(x, kFltMax)) * steps;
+    if (more != 1.f) d *= more;
+    return static_cast<int>(fminf(d, static_cast<float>(kBins - 1)));
   }
-  NLD_DEV double real(float x) const {
-    if (x == top) return 1.0;
-    if (bin(x) == kBins - 1) return 0.0;
-    return exp((static_cast<double>(x) - top_d) * inv_t);
+  // exp((x - top) / T) 2^44 + 2^52, rounded to a whole number, as the bits of the double (kBias + the
+  // weight); kBias where !in, or where x is under `low` and not in.  With y = 16 log2(e) (x - top) / T = k + r,
+  // |r| <= 1/2: 2^(y / 16) = 2^(k / 16) p(r), p the Chebyshev interpolant of degree 5 of 2^(r / 16) with p(0)
+  // set to 1: within 2^-46 of it.  Adding 1.5 2^52 rounds y, adding 2^52 the weight.
+  static constexpr u64 kBias = 0x4330000000000000ull;
+  NLD_DEV u64 biased(float x, bool in) const {
+    double p;
+    const double scaled = parts(fminf(fmaxf(x, low), kFltMax), in, p);
+    return static_cast<u64>(__double_as_longlong(fma(scaled, p, kExp[7])));
   }
-  // exp((x - top) / T) 2^44, rounded, of an x that is not in the last bin.  With y = 16 log2(e) (x - top) / T
-  // = k + r, |r| <= 1/2: 2^(y / 16) = 2^(k / 16) p(r), p the Chebyshev interpolant of degree 5 of 2^(r / 16)
-  // with p(0) set to 1: within 2^-46 of it.  y is rounded, and w converted, by adding 2^52 and more.
-  NLD_DEV u64 fixed(float x) const {
-    constexpr double kRound = 6755399441055744.0;   // 1.5 2^52: whole numbers in the low word
-    const double d = x == top ? 0.0 : static_cast<double>(x) - top_d;
-    const double t = fma(d, s16, kRound);
-    const double r = fma(d, s16, kRound - t);
+  // The same for every logit of a row with plain(): what is under `low` counts as `low`, which has no weight.
+  NLD_DEV u64 biased(float x) const {
+    double p;
+    const double scaled = parts(fmaxf(x, low), true, p);
+    return static_cast<u64>(__double_as_longlong(fma(scaled, p, kExp[7])));
+  }
+  NLD_DEV bool plain() const { return top < kFltMax && fixed(low) == 0; }
+  NLD_DEV double parts(float x, bool in, double& p) const {
+    const double d = static_cast<double>(x) - top_d;
+    const double t = fma(d, s16, kExp[0]);
+    const double r = fma(d, s16, kExp[0] - t);
     const int k = __double2loint(t);
-    double p = fma(r, 1.2716085030349987e-09, 1.4676444621898709e-07);
-    p = fma(r, p, 1.355080777749983e-05);
-    p = fma(r, p, 0.000938384792486206);
-    p = fma(r, p, 0.043321698784996608);
-    p = fma(r, p, 1.0);
+    p = fma(r, kExp[1], kExp[2]);
+    p = fma(r, p, kExp[3]);
+    p = fma(r, p, kExp[4]);
+    p = fma(r, p, kExp[5]);
+    p = fma(r, p, kExp[6]);
     const double m = tab[k & 15];
-    const double scaled = __hiloint2double(__double2hiint(m) + (((k >> 4) + 44) << 20), __double2loint(m));
-    return static_cast<u64>(__double_as_longlong(fma(scaled, p, 4503599627370496.0))) & 0x000fffffffffffffull;
+    const int hi = __double2hiint(m) + (k << 16);
+    return __hiloint2double(in ? hi : 0, __double2loint(m));
   }
+  NLD_DEV u64 fixed(float x) const { return biased(x, true) - kBias; }
 };
+// The same out of line, for code that runs once: a call that samples few logits is bound by fetching its
+// instructions.
+__device__ __noinline__ u64 fixed_weight(const Weigh& w, float x) { return w.fixed(x); }
+__device__ __noinline__ double real_weight(const Weigh& w, float x) {   // not rounded to a whole number
+  double p;
+  const double scaled = w.parts(fminf(fmaxf(x, w.low), kFltMax), true, p);
+  return scaled * p;
+}
 
 template <typename V>
 NLD_DEV V warp_sum(V v) {
@@ -156,7 +187,7 @@ NLD_DEV V warp_scan(V v) {
 // Sum over the threads before this one, and over all.  `red` holds kWarps entries; callable again at
 // once.
 template <typename V>
-NLD_DEV V block_scan(V v, V* red, V& total) {
+__device__ __noinline__ V block_scan(V v, V* red, V& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const V inc = warp_scan(v);
   __syncthreads();
@@ -181,25 +212,33 @@ NLD_DEV uint32_t ld_dsmem_u32(uint32_t addr) {
 
 NLD_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 NLD_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-template <bool kValue>
-struct Flag {
-  static constexpr bool value = kValue;
-};
+NLD_DEV void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+NLD_DEV void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // What a CTA's peers read, and its own scratch.
 struct Shared {
-  uint32_t hist[2][3][kBins];   // [buffer][limb][bin]; counts use limb 0
+  union {
+    uint32_t hist[2][3][kBins];        // [buffer][limb][bin]; counts use limb 0
+    struct {
+      u64 all[kList], weight[kList];   // rank 0, after the searches: the lists of all CTAs, the tokens' weights
+    };
+  };
   u64 range[2][kRanges];        // [buffer]: sums over 32 bins
-  u64 best;                     // the slice's largest key and the complement of its lowest index
+  u64 list[kList];              // key, then the index's complement
   u64 part_mass[kWarps];        // kept mass over the border, ties at it: of each warp's part of the slice
   int part_ties[kWarps];
   double tab[16];
+  Weigh weigh;
   u64 red_m[kWarps];
   int red_c[kWarps];
-  u64 found_before;             // warp 0's findings
-  u64 found_total;
-  int found_at;
+  uint32_t top;                 // the slice's largest key
+  int top_at;                   // the lowest index of the row's largest logit in the slice
+  int listed;                   // tokens of `list` (more: not all are in it)
+  int found_at;                 // warp 0's findings
   uint32_t key_lo, key_hi;
+  u64 found_before, found_with, found_total;
   int at_part, done;            // the sampled token's part, and what lies before that part
   u64 at_before, total;
   long long at_ties;
@@ -207,7 +246,7 @@ struct Shared {
 };
 
 // One row's slice: the 16-byte vectors of it, in shared memory or (slices over the shared memory)
-// straight from global memory.
+// straight from global memory; -inf outside the row.
 template <typename T, bool kStaged>
 struct Slice {
   static constexpr int n = Key<T>::n;
@@ -215,26 +254,36 @@ struct Slice {
   const T* row;
   long long first;    // index of the slice's first logit (a 16-byte boundary; before the row's start by up to n - 1)
   int vocab;
-  NLD_DEV bool whole(int v) const {
+  int whole0, whole1;   // vectors that lie in the row
+  NLD_DEV bool whole(int v) const { return v >= whole0 && v < whole1; }
+  NLD_DEV const uint4* vector(int v) const { return reinterpret_cast<const uint4*>(row + (first + static_cast<long long>(v) * n)); }
+  __device__ __noinline__ uint4 ragged(int v) const {   // a vector at the row's ends
     const long long i0 = first + static_cast<long long>(v) * n;
-    return i0 >= 0 && i0 + n <= vocab;
-  }
-  NLD_DEV uint4 raw(int v) const { return __ldg(reinterpret_cast<const uint4*>(row + (first + static_cast<long long>(v) * n))); }
-  // plain_logit of the logits of vector v, read as `got` where it is whole; -inf outside the row
-  NLD_DEV void plain(int v, const uint4& got, float (&x)[n]) const {
-    if (whole(v)) {
-      Key<T>::unpack(got, x);
+    uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < n; ++e) x[e] = plain_logit(x[e]);
-    } else {
-      const long long i0 = first + static_cast<long long>(v) * n;
-#pragma unroll
-      for (int e = 0; e < n; ++e) x[e] = i0 + e >= 0 && i0 + e < vocab ? plain_logit(to_f32<T>(row[i0 + e])) : -INFINITY;
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (n == 4) {
+        w[i] = i0 + i >= 0 && i0 + i < vocab ? reinterpret_cast<const uint32_t*>(row)[i0 + i] : 0xff800000u;
+      } else {
+        const long long e = i0 + 2 * i;
+        const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
+        const uint32_t lo = e >= 0 && e < vocab ? r[e] : 0xff80u, hi = e + 1 >= 0 && e + 1 < vocab ? r[e + 1] : 0xff80u;
+        w[i] = lo | (hi << 16);
+      }
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  NLD_DEV void get(int v, float (&x)[n]) const {
-    if constexpr (kStaged) Key<T>::unpack(staged[v], x);
-    else plain(v, whole(v) ? raw(v) : make_uint4(0, 0, 0, 0), x);
+  NLD_DEV void get(int q, float (&x)[4]) const {   // the 4 logits of quad q
+    typedef typename Key<T>::Quad Quad;
+    constexpr int per = n / 4;
+    if constexpr (kStaged) {
+      Key<T>::unpack(reinterpret_cast<const Quad*>(staged)[q], x);
+    } else if (whole(q / per)) {
+      Key<T>::unpack(__ldg(reinterpret_cast<const Quad*>(row + (first + static_cast<long long>(q) * 4))), x);
+    } else {
+      const uint4 v = ragged(q / per);
+      Key<T>::unpack(reinterpret_cast<const Quad*>(&v)[per == 1 ? 0 : q % per], x);
+    }
   }
 };
 
@@ -255,255 +304,367 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   // the row's vectors start at the 16-byte boundary at or before it; warp w of the slice has a.part of them
   const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(slice.row) % 16 / sizeof(T));
   slice.first = static_cast<long long>(rank) * (a.part * kWarps * n) - skew;
+  slice.whole0 = slice.first < 0 ? 1 : 0;
+  slice.whole1 = max(slice.whole0, static_cast<int>(max(-1LL, min(static_cast<long long>(a.part) * kWarps, (a.vocab - slice.first) / n))));
   const int v0 = warp * a.part, v1 = v0 + a.part;
-  const uint32_t sh_base = smem_u32(&sh);
+  const int q0 = v0 * (n / 4), q1 = v1 * (n / 4);   // the same in quads of logits
 
-  for (int i = tid; i < 2 * 3 * kBins; i += kThreads) (&sh.hist[0][0][0])[i] = 0;
-  if (tid < 16) sh.tab[tid] = exp2(tid * 0.0625);
-
-  // the largest logit, and the lowest index that has it
-  {
-    float big = -INFINITY;
-    int at = 0x7fffffff;
-    constexpr int kU = 8;   // vectors in flight
-    for (int vb = v0 + lane; vb < v1; vb += 32 * kU) {
-      uint4 got[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if (vb + 32 * u < v1 && slice.whole(vb + 32 * u)) got[u] = slice.raw(vb + 32 * u);
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int v = vb + 32 * u;
-        if (v >= v1) break;
-        float x[n];
-        slice.plain(v, got[u], x);
-        if constexpr (kStaged) reinterpret_cast<uint4*>(smem + kHead)[v] = K::pack(x);
-#pragma unroll
-        for (int e = 0; e < n; ++e)
-          if (x[e] > big) {
-            big = x[e];
-            at = v * n + e;
-          }
-      }
-    }
-    u64 best = (static_cast<u64>(K::of(big)) << 32) |
-               (big == -INFINITY ? 0u : 0xffffffffu - static_cast<uint32_t>(slice.first + at));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const u64 o = __shfl_xor_sync(0xffffffffu, best, off);
-      best = o > best ? o : best;
-    }
-    if (lane == 0) sh.red_m[warp] = best;
-    __syncthreads();
-    if (warp == 0) {
-      best = lane < kWarps ? sh.red_m[lane] : 0;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        const u64 o = __shfl_xor_sync(0xffffffffu, best, off);
-        best = o > best ? o : best;
-      }
-      if (lane == 0) sh.best = best;
-    }
-  }
-  cluster_sync();
-  u64 best = lane < S ? ld_dsmem_u64(dsmem_addr(smem_u32(&sh.best), lane)) : 0;
-#pragma unroll
-  for (int off = 4; off > 0; off >>= 1) {
-    const u64 o = __shfl_xor_sync(0xffffffffu, best, off);
-    best = o > best ? o : best;
-  }
-  best = __shfl_sync(0xffffffffu, best, 0);
-  const uint32_t top_key = static_cast<uint32_t>(best >> 32);
-  const float temperature = a.temperature ? a.temperature[row] : 1.f;
-  if (top_key == K::kInf || !(temperature > 0.f)) {   // (the same for the whole cluster)
-    if (rank == 0 && tid == 0) {
-      a.tokens[row] = top_key == K::kInf ? -1 : static_cast<int>(0xffffffffu - static_cast<uint32_t>(best));
-      if (a.prob) a.prob[row] = top_key == K::kInf ? 0.f : 1.f;
-    }
-    cluster_sync();   // peers may still be reading sh.best
-    return;
-  }
-  Weigh weigh;
-  weigh.init(K::value(top_key), temperature, sh.tab);
-
-  // Border among the tokens with keys over kept_over: the key with which their number (by mass: their mass)
-  // in falling order reaches `limit` (by mass: that share of `total`, which is their mass and `rest`).  False
-  // if none of those with a weight does; else `key`, and in `before` what lies over it.
-  int buf = 0;
-  auto find = [&](auto by_mass, uint32_t kept_over, u64 rest, double limit, uint32_t& key, u64& before, u64& total) -> bool {
-    constexpr bool kMass = decltype(by_mass)::value;
-    uint32_t lo = 0, hi = 0;   // keys of the current bin
-    before = 0;
-    for (int level = 0;; ++level) {
-      uint32_t(*h)[kBins] = sh.hist[buf];
-      int shift = 0;
-      if (level > 0)
-        while (((hi - lo) >> shift) >= kBins) ++shift;
-      for (int v = v0 + lane; v < v1; v += 32) {
-        float x[n];
-        slice.get(v, x);
-#pragma unroll
-        for (int e = 0; e < n; ++e) {
-          int b;
-          bool in;
-          if (level == 0) {
-            b = weigh.bin(x[e]);
-            in = b < kBins - 1 && (!kMass || K::of(x[e]) > kept_over);
-          } else {
-            const uint32_t k = K::of(x[e]);
-            in = k >= lo && k <= hi;
-            b = static_cast<int>((hi - k) >> shift);
-          }
-          if (!in) continue;
-          if constexpr (kMass) {
-            const u64 w = weigh.fixed(x[e]);
-            const uint32_t w2 = static_cast<uint32_t>(w >> 30), w1 = static_cast<uint32_t>(w >> 15) & 0x7fffu;
-            atomicAdd(&h[0][b], static_cast<uint32_t>(w) & 0x7fffu);
-            if (w1) atomicAdd(&h[1][b], w1);
-            if (w2) atomicAdd(&h[2][b], w2);
-          } else {
-            atomicAdd(&h[0][b], 1u);
-          }
-        }
-      }
-      __syncthreads();
-      auto bin_sum = [&](uint32_t base, int b) -> u64 {   // of one CTA, at its shared-window address
-        const uint32_t p = base + static_cast<uint32_t>(reinterpret_cast<uint8_t*>(&h[0][0]) - smem) + b * 4;
-        u64 s = ld_dsmem_u32(p);
-        if constexpr (kMass)
-          s += (static_cast<u64>(ld_dsmem_u32(p + kBins * 4)) << 15) + (static_cast<u64>(ld_dsmem_u32(p + 2 * kBins * 4)) << 30);
-        return s;
-      };
-      const uint32_t own = dsmem_addr(sh_base, rank);
-      for (int r = warp; r < kRanges; r += kWarps) {
-        const u64 s = warp_sum(bin_sum(own, r * 32 + lane));
-        if (lane == 0) sh.range[buf][r] = s;
-      }
-      cluster_sync();
-      // the other buffer was last read before this barrier
-      for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[buf ^ 1][0][0])[i] = 0;
-      if (warp == 0) {
-        u64 s = 0;
-        const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uint8_t*>(&sh.range[buf][lane]) - smem);
-#pragma unroll
-        for (int q = 0; q < kMaxS; ++q)
-          if (q < S) s += ld_dsmem_u64(dsmem_addr(sh_base, q) + at);
-        u64 inc = warp_scan(s);
-        if (level == 0) {
-          total = __shfl_sync(0xffffffffu, inc, 31) + rest;
-          if (kMass) limit *= static_cast<double>(total);   // (warp 0 alone compares with it)
-        }
-        auto reached = [&](u64 c) { return static_cast<double>(before + c) >= limit; };
-        uint32_t m = __ballot_sync(0xffffffffu, reached(inc));
-        int found = -1;
-        if (m) {
-          const int r = __ffs(m) - 1;
-          const u64 base = __shfl_sync(0xffffffffu, inc - s, r);
-          u64 t = 0;
-#pragma unroll
-          for (int q = 0; q < kMaxS; ++q)
-            if (q < S) t += bin_sum(dsmem_addr(sh_base, q), r * 32 + lane);
-          inc = warp_scan(t);
-          m = __ballot_sync(0xffffffffu, reached(base + inc));
-          const int l = __ffs(m) - 1;
-          before += base + __shfl_sync(0xffffffffu, inc - t, l);
-          found = r * 32 + l;
-        }
-        // the keys of that bin
-        uint32_t klo = 0, khi = 0;
-        if (found >= 0 && level == 0) {
-          // lowest key of a bin <= b, by 32 probes at a time: keys (from, to], `to` is one
-          auto lowest = [&](int b) -> uint32_t {
-            uint32_t from = K::kInf, to = top_key;
-            while (to - from > 1) {
-              const uint32_t step = (to - from + 31) / 32;
-              const u64 probe64 = static_cast<u64>(from) + static_cast<u64>(step) * (lane + 1);
-              const uint32_t probe = probe64 < to ? static_cast<uint32_t>(probe64) : to;
-              const int first = __ffs(__ballot_sync(0xffffffffu, weigh.bin(K::value(probe)) <= b)) - 1;
-              const uint32_t got = __shfl_sync(0xffffffffu, probe, first);
-              from = first > 0 ? __shfl_sync(0xffffffffu, probe, first - 1) : from;
-              to = got;
-            }
-            return to;
-          };
-          klo = lowest(found);
-          klo = klo > kept_over ? klo : kept_over + 1;
-          khi = found > 0 ? lowest(found - 1) - 1 : top_key;
-        } else if (found >= 0) {
-          khi = hi - (static_cast<uint32_t>(found) << shift);
-          klo = khi - lo < (1u << shift) ? lo : khi - ((1u << shift) - 1);
-        }
-        if (lane == 0) {
-          sh.found_at = found;
-          sh.found_before = before;
-          sh.found_total = total;
-          sh.key_lo = klo;
-          sh.key_hi = khi;
-        }
-      }
-      __syncthreads();
-      buf ^= 1;
-      before = sh.found_before;
-      total = sh.found_total;
-      lo = sh.key_lo;
-      hi = sh.key_hi;
-      if (sh.found_at < 0) return false;
-      if (lo == hi) {
-        key = lo;
-        return true;
-      }
-    }
+  // a word of CTA q's Shared, at the place of `p` in this one's
+  auto peer64 = [&](const void* p, int q) -> u64 {
+    return S == 1 ? *static_cast<const volatile u64*>(p) : ld_dsmem_u64(dsmem_addr(smem_u32(p), q));
+  };
+  auto peer32 = [&](const void* p, int q) -> uint32_t {
+    return S == 1 ? *static_cast<const volatile uint32_t*>(p) : ld_dsmem_u32(dsmem_addr(smem_u32(p), q));
+  };
+  auto row_sync = [&]() {
+    if (S == 1) __syncthreads();
+    else cluster_sync();
   };
 
+  const float temperature = a.temperature ? a.temperature[row] : 1.f;
+  const int k = a.top_k ? a.top_k[row] : 0;
+  const float p = a.top_p ? a.top_p[row] : 1.f;
+  const float mp = a.min_p ? a.min_p[row] : 0.f;
+  const float uf = a.u[row];
+  if (tid < 16) sh.tab[tid] = __hiloint2double(__double2hiint(kTab[tid]) - (tid << 16), __double2loint(kTab[tid]));
+  if (tid == 0) {
+    sh.listed = 0;
+    sh.top_at = 0x7fffffff;
+  }
+  const bool by_k = k > 0 && k < a.vocab, by_p = p < 1.f;
+  auto clear = [&](int buffer) {
+    for (int i = tid; i < 3 * kBins / 4; i += kThreads) reinterpret_cast<uint4*>(&sh.hist[buffer][0][0])[i] = make_uint4(0, 0, 0, 0);
+  };
+  if (by_k || by_p) clear(0);
+
+  // the largest logit
+  {
+    float big = -INFINITY;
+    const int w0 = max(v0, slice.whole0), w1 = min(v1, slice.whole1);
+    if constexpr (kStaged) {   // all of the slice in flight; a thread reads back what it copied itself
+      uint4* const to = reinterpret_cast<uint4*>(smem + kHead);
+      for (int v = w0 + lane; v < w1; v += 32) cp_async16(to + v, slice.vector(v));
+      cp_async_wait();
+      for (int v = w0 + lane; v < w1; v += 32) big = fmaxf(big, K::most(to[v]));
+    } else {
+#pragma unroll 4
+      for (int v = w0 + lane; v < w1; v += 32) big = fmaxf(big, K::most(__ldg(slice.vector(v))));
+    }
+    if (!slice.whole(0) || !slice.whole(kWarps * a.part - 1))   // a row's ends
+      for (int v = v0 + lane; v < v1; v += 32)
+        if (!slice.whole(v)) {
+          const uint4 got = slice.ragged(v);
+          if constexpr (kStaged) reinterpret_cast<uint4*>(smem + kHead)[v] = got;
+          big = fmaxf(big, K::most(got));
+        }
+    const uint32_t key = __reduce_max_sync(0xffffffffu, K::of(big));
+    if (lane == 0) sh.red_c[warp] = static_cast<int>(key);
+    __syncthreads();
+    if (warp == 0) {
+      const uint32_t all = __reduce_max_sync(0xffffffffu, lane < kWarps ? static_cast<uint32_t>(sh.red_c[lane]) : 0u);
+      if (lane == 0) sh.top = all;
+    }
+  }
+  row_sync();
+  const uint32_t top_key = __reduce_max_sync(0xffffffffu, lane < S ? peer32(&sh.top, lane) : 0u);
+  if (top_key == K::kInf || !(temperature > 0.f) || k == 1 || p <= 0.f) {   // (the same for the whole cluster)
+    if (top_key != K::kInf) {   // the likeliest token alone: the lowest index with the largest logit
+      const float top = K::value(top_key);
+      for (int q = q0 + lane; q < q1; q += 32) {
+        float x[4];
+        slice.get(q, x);
+        const int at = x[0] == top ? 0 : x[1] == top ? 1 : x[2] == top ? 2 : x[3] == top ? 3 : -1;
+        if (at >= 0) {
+          atomicMin(&sh.top_at, static_cast<int>(slice.first + static_cast<long long>(q) * 4 + at));
+          break;   // this thread's later ones have higher indexes
+        }
+      }
+    }
+    row_sync();
+    if (rank == 0 && warp == 0) {
+      const int at = __reduce_min_sync(0xffffffffu, lane < S ? static_cast<int>(peer32(&sh.top_at, lane)) : 0x7fffffff);
+      if (lane == 0) {
+        a.tokens[row] = top_key == K::kInf ? -1 : at;
+        if (a.prob) a.prob[row] = top_key == K::kInf ? 0.f : 1.f;
+      }
+    }
+    row_sync();   // peers' shared memory may still be read
+    return;
+  }
+  if (tid == 0) sh.weigh.init(K::value(top_key), temperature, sh.tab);
+  __syncthreads();
+  Weigh weigh = sh.weigh;
+  weigh.tab = sh.tab;   // (known to be shared memory)
+  const double u = uf > 0.f ? static_cast<double>(fminf(uf, 0.99999994f)) : 0.0;
+  const u64 least = mp > 0.f ? static_cast<u64>(ceil(static_cast<double>(fminf(mp, 1.f)) * kOne)) : 0;
+
+  // ------------------------------------------------------------------ the border --
   // kept: keys over `border`, and the first `ties` tokens at it
   uint32_t border = K::kInf;
   long long ties = a.vocab;
-  u64 over = 0, total = 0;
-  const int k = a.top_k ? a.top_k[row] : 0;
-  if (k > 0 && k < a.vocab && find(Flag<false>(), K::kInf, 0, k, border, over, total)) ties = k - static_cast<long long>(over);
-  const float p = a.top_p ? a.top_p[row] : 1.f;
-  if (p <= 0.f) {   // p of nothing: the likeliest token alone
-    border = top_key;
-    ties = 1;
-  } else if (p < 1.f) {
-    const u64 at_border = border == K::kInf ? 0 : weigh.fixed(K::value(border)) * static_cast<u64>(ties);
-    uint32_t key = border;
-    const bool below = find(Flag<true>(), border, at_border, p, key, over, total);
-    const double limit = static_cast<double>(p) * static_cast<double>(total);
-    if (below) ties = a.vocab;
-    else over = total - at_border;
-    border = key;
+  auto over_border = [&]() {   // logits from here on are over the border and have a weight
+    return border >= top_key ? NAN : fmaxf(weigh.low, K::value(border + 1));   // (NaN: none are)
+  };
+  bool mass = !by_k;       // what is searched for: by number first, then by mass among the kept
+  int level = 0, buf = 0;
+  u64 before = 0, rest = 0, rest_w = 0;   // over the bin; mass of the ties at the top-k border, and of one of them
+  double limit = by_k ? k : p;            // level 0 by mass: a share of the total
+  uint32_t lo = 0, hi = 0;                // keys of the bin (levels 1 and up)
+  while (by_k || by_p) {
+    // One level: tokens over the border (level 0) or with keys lo..hi, in steps of 2^shift; their numbers or masses
+    // by bin, and the bin with which the sum reaches the limit.
+    uint32_t(*h)[kBins] = sh.hist[buf];
+    const int shift = level > 0 ? max(0, 22 - __clz(hi - lo)) : 0;   // (hi - lo) >> shift < 2^10
+    {
+      const float from = level == 0 ? over_border() : K::value(lo), to = level == 0 ? INFINITY : K::value(hi);
+      for (int q = q0 + lane; q < q1; q += 32) {
+        float x[4];
+        slice.get(q, x);
+        bool in[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) in[e] = x[e] >= from && x[e] <= to;
+        if (!(in[0] || in[1] || in[2] || in[3])) continue;
+        u64 w[4];
+        int bin[4];
+        if (mass) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = weigh.biased(x[e], in[e]) - Weigh::kBias;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bin[e] = level == 0 ? weigh.bin(x[e]) : static_cast<int>((hi - K::of(x[e])) >> shift);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!in[e]) continue;
+          uint32_t* const at = &h[0][0] + bin[e];
+          if (mass) {
+            const uint32_t w2 = static_cast<uint32_t>(w[e] >> 30), w1 = static_cast<uint32_t>(w[e] >> 15) & 0x7fffu;
+            atomicAdd(at, static_cast<uint32_t>(w[e]) & 0x7fffu);
+            if (w1) atomicAdd(at + kBins, w1);
+            if (w2) atomicAdd(at + 2 * kBins, w2);
+          } else {
+            atomicAdd(at, 1u);
+          }
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int r = warp; r < kRanges; r += kWarps) {
+      const int b = r * 32 + lane;   // (counts: the other limbs are 0)
+      const u64 s = warp_sum(h[0][b] + (static_cast<u64>(h[1][b]) << 15) + (static_cast<u64>(h[2][b]) << 30));
+      if (lane == 0) sh.range[buf][r] = s;
+    }
+    row_sync();
+    // the other buffer was last read before this barrier
+    clear(buf ^ 1);
+    if (warp == 0) {
+      u64 s = 0;
+#pragma unroll
+      for (int q = 0; q < kMaxS; ++q)
+        if (q < S) s += peer64(&sh.range[buf][lane], q);
+      u64 inc = warp_scan(s);
+      const u64 total = __shfl_sync(0xffffffffu, inc, 31) + rest;
+      double reach = limit;
+      if (mass && level == 0) reach *= static_cast<double>(total);
+      auto reached = [&](u64 c) { return static_cast<double>(before + c) >= reach; };
+      uint32_t m = __ballot_sync(0xffffffffu, reached(inc));
+      int found = -1;
+      u64 with = 0, ahead = before;
+      if (m) {
+        const int r = __ffs(m) - 1;
+        const u64 base = __shfl_sync(0xffffffffu, inc - s, r);
+        const int b = r * 32 + lane;
+        u64 t = 0;
+#pragma unroll
+        for (int q = 0; q < kMaxS; ++q)
+          if (q < S)
+            t += peer32(&h[0][b], q) + (static_cast<u64>(peer32(&h[1][b], q)) << 15) + (static_cast<u64>(peer32(&h[2][b], q)) << 30);
+        inc = warp_scan(t);
+        m = __ballot_sync(0xffffffffu, reached(base + inc));
+        const int l = __ffs(m) - 1;
+        with = before + base + __shfl_sync(0xffffffffu, inc, l);
+        ahead += base + __shfl_sync(0xffffffffu, inc - t, l);
+        found = r * 32 + l;
+      }
+      uint32_t klo = 0, khi = 0;
+      if (found >= 0 && level == 0) {
+        // lowest keys of bins <= found and of bins < found, by 32 probes at a time: keys (none, most], `most` is one
+        khi = top_key;
+#pragma unroll 1
+        for (int b = found; b >= max(0, found - 1); --b) {
+          uint32_t none = max(border, K::of(weigh.low) - 1), most = top_key;   // (keys under weigh.low: no weight)
+          while (most - none > 1) {
+            const uint32_t step = (most - none + 31) / 32;
+            const u64 probe64 = static_cast<u64>(none) + static_cast<u64>(step) * (lane + 1);
+            const uint32_t probe = probe64 < most ? static_cast<uint32_t>(probe64) : most;
+            const int first = __ffs(__ballot_sync(0xffffffffu, weigh.bin(K::value(probe)) <= b)) - 1;
+            most = __shfl_sync(0xffffffffu, probe, first);
+            if (first > 0) none = __shfl_sync(0xffffffffu, probe, first - 1);
+          }
+          if (b == found) klo = most;
+          else khi = most - 1;
+        }
+      } else if (found >= 0) {
+        khi = hi - (static_cast<uint32_t>(found) << shift);
+        klo = khi - lo < (1u << shift) ? lo : khi - ((1u << shift) - 1);
+      }
+      if (lane == 0) {
+        sh.found_at = found;
+        sh.found_before = ahead;
+        sh.found_with = with;
+        sh.found_total = total;
+        sh.key_lo = klo;
+        sh.key_hi = khi;
+      }
+    }
+    __syncthreads();
+    buf ^= 1;
+    const bool found = sh.found_at >= 0;
+    if (mass && level == 0) limit *= static_cast<double>(sh.found_total);
+    before = found ? sh.found_before : sh.found_total - rest;
+    lo = sh.key_lo;
+    hi = sh.key_hi;
+    if (found && level == 0 && (mass || sh.found_with <= kList)) {
+      // the tokens down to the bin's last key into the lists
+      const float from = K::value(lo);
+      for (int q = q0 + lane; q < q1 && *static_cast<volatile int*>(&sh.listed) <= kList; q += 32) {
+        float x[4];
+        slice.get(q, x);
+        if (!(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (x[e] >= from) {
+            const int at = atomicAdd(&sh.listed, 1);
+            if (at < kList)
+              sh.list[at] = (static_cast<u64>(K::of(x[e])) << 32) |
+                            (0xffffffffu - static_cast<uint32_t>(slice.first + static_cast<long long>(q) * 4 + e));
+          }
+      }
+      row_sync();
+      const int count = __reduce_add_sync(0xffffffffu, lane < S ? static_cast<int>(peer32(&sh.listed, lane)) : 0);
+      if (count <= kList) {   // (the same in every CTA)
+        if (rank == 0) {
+          int first = 0;   // every thread an entry of one of the lists
+          for (int q = 0; q < S; ++q) {
+            const int c = static_cast<int>(peer32(&sh.listed, q));
+            if (tid >= first && tid < first + c) sh.all[tid] = peer64(&sh.list[tid - first], q);
+            first += c;
+          }
+          __syncthreads();
+        }
+        if (S > 1) cluster_arrive();   // the lists are read
+        if (rank == 0) {
+          // 2 to 16 lanes an entry, each against its share of the others
+          int lanes = 16;
+          while (lanes * count > kThreads) lanes >>= 1;
+          const int at = tid / lanes, sub = tid % lanes;
+          const bool in = at < count;
+          const u64 mine = in ? sh.all[at] : 0;
+          const float x = K::value(static_cast<uint32_t>(mine >> 32));
+          const u64 w = in ? fixed_weight(sh.weigh, x) : 0;
+          if (in && sub == 0) sh.weight[at] = w;
+          __syncthreads();
+          int rank_of = 0;
+          u64 over = 0;
+          if (in)
+            for (int j = sub; j < count; j += lanes)
+              if (sh.all[j] > mine) {
+                ++rank_of;
+                over += sh.weight[j];
+              }
+          for (int off = 1; off < lanes; off <<= 1) {
+            rank_of += __shfl_xor_sync(0xffffffffu, rank_of, off);
+            over += __shfl_xor_sync(0xffffffffu, over, off);
+          }
+          bool keep = in && (mass || rank_of < k);
+          u64 total;
+          if (!mass) {
+            block_scan(keep && sub == 0 ? w : 0, sh.red_m, total);
+            limit = (by_p ? static_cast<double>(p) : 2.0) * static_cast<double>(total);
+          }
+          keep = keep && (rank_of == 0 || static_cast<double>(over) < limit) && w >= least;
+          __syncthreads();   // the weights are read
+          if (in && sub == 0) sh.weight[at] = keep ? w : 0;
+          block_scan(keep && sub == 0 ? w : 0, sh.red_m, total);   // (its barriers publish the kept weights)
+          const uint32_t code = static_cast<uint32_t>(mine);   // falls as the index rises
+          u64 sum = 0;
+          if (in)
+            for (int j = sub; j < count; j += lanes)
+              if (static_cast<uint32_t>(sh.all[j]) > code) sum += sh.weight[j];
+          for (int off = 1; off < lanes; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+          const double target = u * static_cast<double>(total);
+          if (keep && sub == 0 && static_cast<double>(sum) <= target && static_cast<double>(sum + w) > target) {
+            a.tokens[row] = static_cast<int>(0xffffffffu - code);
+            if (a.prob) a.prob[row] = static_cast<float>(real_weight(sh.weigh, x) / static_cast<double>(total));
+          }
+        }
+        if (S > 1) cluster_wait();
+        return;
+      }
+    }
+    ++level;
+    if (found && lo != hi) continue;
+    if (found) border = lo;
+    // (not found: by number, every token with a weight is kept; by mass, the border of top-k stays)
+    if (!mass) {
+      if (found) ties = k - static_cast<long long>(before);
+      if (!by_p) break;
+      mass = true;
+      level = 0;
+      limit = p;
+      before = 0;
+      rest_w = border == K::kInf ? 0 : fixed_weight(sh.weigh, K::value(border));
+      rest = rest_w ? rest_w * static_cast<u64>(ties) : 0;
+      continue;
+    }
     // a tie is kept while the mass before it is under the limit
-    const u64 w = border == K::kInf ? 0 : weigh.fixed(K::value(border));
-    if (w > 0) {
-      long long c = static_cast<long long>((limit - static_cast<double>(over)) / static_cast<double>(w));
+    if (found) {
+      ties = a.vocab;
+      rest_w = fixed_weight(sh.weigh, K::value(border));
+    }
+    if (rest_w > 0) {
+      long long c = static_cast<long long>((limit - static_cast<double>(before)) / static_cast<double>(rest_w));
       c = c < 0 ? 0 : c;
-      while (c > 0 && static_cast<double>(over + static_cast<u64>(c - 1) * w) >= limit) --c;
-      while (c < a.vocab && static_cast<double>(over + static_cast<u64>(c) * w) < limit) ++c;
+      while (c > 0 && static_cast<double>(before + static_cast<u64>(c - 1) * rest_w) >= limit) --c;
+      while (c < a.vocab && static_cast<double>(before + static_cast<u64>(c) * rest_w) < limit) ++c;
       ties = c < ties ? c : ties;
     }
+    break;
   }
-  const float mp = a.min_p ? a.min_p[row] : 0.f;
-  const double least = mp > 0.f ? static_cast<double>(fminf(mp, 1.f)) * kOne : 0.0;
-  auto kept_mass = [&](float x) -> u64 {   // of a token over the border
-    if (weigh.bin(x) == kBins - 1) return 0;
-    const u64 w = weigh.fixed(x);
-    return static_cast<double>(w) >= least ? w : 0;
-  };
-  const u64 border_w = border == K::kInf ? 0 : kept_mass(K::value(border));
 
+  // ------------------------------------------------------------------- the token --
+  const float border_x = K::value(border);
+  const float cut = over_border();
+  const bool filtered = border != K::kInf || least > 0 || !weigh.plain();
+  u64 border_w = 0;
+  if (border != K::kInf && border_x >= weigh.low) {
+    border_w = fixed_weight(sh.weigh, border_x);
+    border_w = border_w >= least ? border_w : 0;
+  }
   // mass over the border and ties of each warp's part of the slice
   {
     u64 s = 0;
     int c = 0;
-    for (int v = v0 + lane; v < v1; v += 32) {
-      float x[n];
-      slice.get(v, x);
+    if (!filtered) {
+      int quads = 0;
+      for (int q = q0 + lane; q < q1; q += 32, ++quads) {
+        float x[4];
+        slice.get(q, x);
 #pragma unroll
-      for (int e = 0; e < n; ++e) {
-        const uint32_t key = K::of(x[e]);
-        if (key > border) s += kept_mass(x[e]);
-        c += key == border;
+        for (int e = 0; e < 4; ++e) s += weigh.biased(x[e]);
+      }
+      s -= static_cast<u64>(quads * 4) * Weigh::kBias;
+    } else {
+      for (int q = q0 + lane; q < q1; q += 32) {
+        float x[4];
+        slice.get(q, x);
+        for (int e = 0; e < 4; ++e) c += x[e] == border_x;
+        if (!(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= cut)) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const u64 w = weigh.biased(x[e], x[e] >= cut) - Weigh::kBias;
+          s += w >= least ? w : 0;
+        }
       }
     }
     s = warp_sum(s);
@@ -513,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       sh.part_ties[warp] = c;
     }
   }
-  cluster_sync();
+  row_sync();
   if (warp == 0) {   // the part with the token: a lane has up to 4 of the parts in a row
     const int per = S >= 2 ? S / 2 : 1;
     u64 m[4];
@@ -524,9 +685,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       m[j] = 0;
       t[j] = 0;
       if (j < per && part < S * kWarps) {
-        const uint32_t peer = dsmem_addr(sh_base, part / kWarps);
-        m[j] = ld_dsmem_u64(peer + static_cast<uint32_t>(offsetof(Shared, part_mass)) + (part % kWarps) * 8);
-        t[j] = static_cast<int>(ld_dsmem_u32(peer + static_cast<uint32_t>(offsetof(Shared, part_ties)) + (part % kWarps) * 4));
+        m[j] = peer64(&sh.part_mass[part % kWarps], part / kWarps);
+        t[j] = static_cast<int>(peer32(&sh.part_ties[part % kWarps], part / kWarps));
       }
       t_sum += t[j];
     }
@@ -542,21 +702,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       t_before += t[j];
     }
     const u64 inc = warp_scan(sum);
-    total = __shfl_sync(0xffffffffu, inc, 31);
-    const float uf = a.u[row];
-    const double target = (uf > 0.f ? static_cast<double>(fminf(uf, 0.99999994f)) : 0.0) * static_cast<double>(total);
+    const u64 total = __shfl_sync(0xffffffffu, inc, 31);
+    const double target = u * static_cast<double>(total);
     const int at = __ffs(__ballot_sync(0xffffffffu, static_cast<double>(inc) > target)) - 1;
     if (lane == at) {
-      u64 before = inc - sum;
+      u64 ahead = inc - sum;
       int j = 0;
 #pragma unroll
       for (int i = 0; i < 3; ++i)
-        if (j == i && static_cast<double>(before + m[i]) <= target) {
-          before += m[i];
+        if (j == i && static_cast<double>(ahead + m[i]) <= target) {
+          ahead += m[i];
           ++j;
         }
       sh.at_part = lane * per + j;
-      sh.at_before = before;
+      sh.at_before = ahead;
       sh.at_ties = j == 0 ? tb[0] : j == 1 ? tb[1] : j == 2 ? tb[2] : tb[3];
       sh.total = total;
       sh.target = target;
@@ -564,57 +723,59 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
   }
   __syncthreads();
-  cluster_arrive();   // this CTA has read what it needs of its peers
-  const int at_part = sh.at_part % kWarps;
+  if (S > 1) cluster_arrive();   // this CTA has read what it needs of its peers
   if (sh.at_part / kWarps == rank) {
-    // the token's part once more, a vector per thread
-    u64 before = sh.at_before;
-    long long ties_before = sh.at_ties;
+    // the token's part once more, a quad per thread
+    const int qa = sh.at_part % kWarps * (a.part * (n / 4)), qb = qa + a.part * (n / 4);
+    u64 ahead = sh.at_before;
+    long long ties_ahead = sh.at_ties;
     const double target = sh.target;
-    for (int i0 = 0; i0 < a.part; i0 += kThreads) {
-      const bool in = i0 + tid < a.part;
-      const int v = at_part * a.part + i0 + tid;
-      float x[n];
-      u64 w[n];
+    for (int qi = qa; qi < qb; qi += kThreads) {
+      const int q = qi + tid;
+      float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      u64 w[4];
       int c = 0;
-      if (in) slice.get(v, x);
+      if (q < qb) slice.get(q, x);
 #pragma unroll
-      for (int e = 0; e < n; ++e) c += in && K::of(x[e]) == border;
-      int n_ties;
-      int tie = block_scan(c, sh.red_c, n_ties);
+      for (int e = 0; e < 4; ++e) c += q < qb && x[e] == border_x;
+      int n_ties = 0, tie = 0;
+      if (filtered) tie = block_scan(c, sh.red_c, n_ties);
       u64 s = 0;
 #pragma unroll
-      for (int e = 0; e < n; ++e) {
+      for (int e = 0; e < 4; ++e) {
         w[e] = 0;
-        if (in) {
-          const uint32_t key = K::of(x[e]);
-          if (key > border) w[e] = kept_mass(x[e]);
-          if (key == border && ties_before + tie++ < ties) w[e] = border_w;
+        if (x[e] >= cut) {
+          w[e] = fixed_weight(sh.weigh, x[e]);
+          w[e] = w[e] >= least ? w[e] : 0;
         }
+        if (filtered && q < qb && x[e] == border_x && ties_ahead + tie++ < ties) w[e] = border_w;
         s += w[e];
       }
-      u64 mass;
-      u64 sum = before + block_scan(s, sh.red_m, mass);
+      u64 part_mass;
+      u64 sum = ahead + block_scan(s, sh.red_m, part_mass);
       if (static_cast<double>(sum) <= target && static_cast<double>(sum + s) > target) {   // one thread's
-        bool open = true;
-#pragma unroll
-        for (int e = 0; e < n; ++e) {
-          sum += w[e];
-          if (open && static_cast<double>(sum) > target) {
-            open = false;
-            a.tokens[row] = static_cast<int>(slice.first + static_cast<long long>(v) * n + e);
-            if (a.prob) a.prob[row] = static_cast<float>(weigh.real(x[e]) * kOne / static_cast<double>(sh.total));
-          }
+        int e = 0;
+        while (static_cast<double>(sum + w[0]) <= target) {   // (its sum exceeds the target: e stays under 4)
+          sum += w[0];
+          w[0] = w[1];
+          w[1] = w[2];
+          w[2] = w[3];
+          x[0] = x[1];
+          x[1] = x[2];
+          x[2] = x[3];
+          ++e;
         }
+        a.tokens[row] = static_cast<int>(slice.first + static_cast<long long>(q) * 4 + e);
+        if (a.prob) a.prob[row] = static_cast<float>(real_weight(sh.weigh, x[0]) / static_cast<double>(sh.total));
         sh.done = 1;
       }
       __syncthreads();
       if (sh.done) break;
-      before += mass;
-      ties_before += n_ties;
+      ahead += part_mass;
+      ties_ahead += n_ties;
     }
   }
-  cluster_wait();
+  if (S > 1) cluster_wait();
 }
 
 template <typename T>
