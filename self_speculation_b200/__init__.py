@@ -13,6 +13,7 @@ from typing import Optional, Sequence
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libnld.so")
+OPERATORS_PATH = os.path.join(PKG_DIR, "_operators.so")
 HEADER = os.path.join(os.path.dirname(PKG_DIR), "include", "nld.h")
 
 NLD_F32, NLD_BF16, NLD_E4M3 = 0, 1, 2
@@ -339,40 +340,27 @@ def nld_lm_head_argmax_static(hidden, lm_weight, rms_eps: float, argmax_out, con
 # -- operators around the paged cache ---------------------------------------------------------
 
 
-def _check_tensors(named) -> None:
-    """named: (name, tensor or None, dtype or dtypes, shape or None) of contiguous tensors on the current
-    device."""
-    import torch
-    dev = torch.cuda.current_device()
-    for name, t, dt, shape in named:
-        if t is None:
-            continue
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be on the current CUDA device ({dev})")
-        if t.dtype != dt if not isinstance(dt, tuple) else t.dtype not in dt:
-            raise ValueError(f"{name} must be {dt}, not {t.dtype}")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+_entries = None   # the loaded _operators module
 
 
-def _done(lib, status: int) -> None:
+def _native():
+    """The extension module that checks the tensors and calls libnld.so (csrc/bind_operators.cpp)."""
+    global _entries
+    if _entries is None:
+        import torch  # noqa: F401  (the extension needs its libraries loaded)
+        load_library()
+        try:
+            from . import _operators as module
+        except ImportError as e:
+            raise RuntimeError(f"{OPERATORS_PATH} cannot be loaded ({e}): build it with "
+                               "`python -m self_speculation_b200.build`") from e
+        _entries = module
+    return _entries
+
+
+def _done(status: int) -> None:
     if status != 0:
-        raise NldError(status, lib.nld_last_error(None).decode())
-
-
-def _token_rows(name: str, t, batch: int, m: int, heads: int, hd: int, dtype):
-    """Elements between the token rows of t [batch, m, heads, hd] (heads contiguous, one distance
-    between all tokens)."""
-    import torch
-    if t.get_device() != torch.cuda.current_device() or t.dtype != dtype or t.shape != (batch, m, heads, hd):
-        raise ValueError(f"{name} must be a {dtype} tensor [{batch}, {m}, {heads}, {hd}] on the current CUDA device")
-    s = t.stride()
-    ld = s[1] if m > 1 else s[0] if batch > 1 else heads * hd
-    if (s[3] != 1 or (heads > 1 and s[2] != hd) or (m > 1 and batch > 1 and s[0] != m * s[1])):
-        raise ValueError(f"{name}: the heads of a token must be contiguous and the tokens evenly spaced")
-    return ld
+        raise NldError(status, load_library().nld_last_error(None).decode())
 
 
 def nld_qk_norm_rope(q, k, v, q_gain, k_gain, rms_eps: float, rope, lens, q_out, kv_pool, page_table,
@@ -384,31 +372,8 @@ def nld_qk_norm_rope(q, k, v, q_gain, k_gain, rms_eps: float, rope, lens, q_out,
     q_out [B, m, Hq, hd], kv_pool [n_pages, 2, Hkv, 64, hd] fp32, bf16 or float8_e4m3fn (with
     k_scale and v_scale [Hkv] fp32), page_table [B, pps] int32, rows [B] int32 live rows per
     sequence (None: all m), err [1] int32 device error word."""
-    import torch
-    lib = load_library()
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q [B, m, Hq, hd] and k [B, m, Hkv, hd] expected")
-    B, m, Hq, hd = q.shape
-    Hkv = k.shape[2]
-    dt = q.dtype
-    if dt != torch.bfloat16 and dt != torch.float32:
-        raise ValueError("q must be bfloat16 or float32")
-    ld = [_token_rows(n, t, B, m, h, hd, dt) for n, t, h in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv))]
-    kinds = {torch.float32: NLD_F32, torch.bfloat16: NLD_BF16, torch.float8_e4m3fn: NLD_E4M3}
-    if rope.dim() != 3 or page_table.dim() != 2 or kv_pool.dim() != 5:
-        raise ValueError("rope [positions, hd/2, 2], page_table [B, pps] and kv_pool [n_pages, 2, Hkv, 64, hd] expected")
-    pps, n_pages = page_table.shape[1], kv_pool.shape[0]
-    _check_tensors((("q_gain", q_gain, dt, (hd,)), ("k_gain", k_gain, dt, (hd,)),
-                    ("rope", rope, torch.float32, (rope.shape[0], hd // 2, 2)), ("lens", lens, torch.int32, (B,)),
-                    ("rows", rows, torch.int32, (B,)), ("q_out", q_out, dt, (B, m, Hq, hd)),
-                    ("kv_pool", kv_pool, tuple(kinds), (n_pages, 2, Hkv, 64, hd)),
-                    ("k_scale", k_scale, torch.float32, (Hkv,)), ("v_scale", v_scale, torch.float32, (Hkv,)),
-                    ("page_table", page_table, torch.int32, (B, pps)), ("err", err, torch.int32, None)))
-    _done(lib, lib.nld_qk_norm_rope(
-        _ptr(q), ld[0], _ptr(k), ld[1], _ptr(v), ld[2], kinds[dt], _ptr(q_gain), _ptr(k_gain), rms_eps, _ptr(rope),
-        rope.shape[0], position_offset, _ptr(lens), _ptr(rows), B, m, Hq, Hkv, hd, _ptr(q_out), _ptr(kv_pool),
-        kinds[kv_pool.dtype], _ptr(k_scale), _ptr(v_scale), _ptr(page_table), pps, n_pages, _ptr(err),
-        _current_stream(stream)))
+    _done(_native().qk_norm_rope(q, k, v, q_gain, k_gain, rms_eps, rope, lens, q_out, kv_pool, page_table,
+                                 position_offset, rows, k_scale, v_scale, err, stream))
 
 
 def nld_attention_q8(q, kv_pool, k_scale, v_scale, page_table, lens, block_size: int, max_len: int, out, err=None,
@@ -416,19 +381,7 @@ def nld_attention_q8(q, kv_pool, k_scale, v_scale, page_table, lens, block_size:
     """nld_attention over an e4m3 cache: kv_pool [n_pages, 2, Hkv, 64, 128] float8_e4m3fn, k_scale
     and v_scale [Hkv] fp32; q [B, m, Hq, 128] bf16, page_table [B, pps] int32, lens [B] int32, out
     like q, err [1] int32 device error word."""
-    import torch
-    lib = load_library()
-    if q.dim() != 4 or kv_pool.dim() != 5 or page_table.dim() != 2:
-        raise ValueError("q [B, m, Hq, hd], kv_pool [n_pages, 2, Hkv, 64, hd] and page_table [B, pps] expected")
-    B, m, Hq, hd = q.shape
-    n_pages, Hkv, pps = kv_pool.shape[0], kv_pool.shape[2], page_table.shape[1]
-    _check_tensors((("q", q, torch.bfloat16, None), ("kv_pool", kv_pool, torch.float8_e4m3fn, (n_pages, 2, Hkv, 64, hd)),
-                    ("k_scale", k_scale, torch.float32, (Hkv,)), ("v_scale", v_scale, torch.float32, (Hkv,)),
-                    ("page_table", page_table, torch.int32, (B, pps)), ("lens", lens, torch.int32, (B,)),
-                    ("out", out, torch.bfloat16, q.shape), ("err", err, torch.int32, None)))
-    _done(lib, lib.nld_attention_q8(_ptr(q), _ptr(kv_pool), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), pps, n_pages,
-                                    _ptr(lens), B, m, Hq, Hkv, hd, block_size, max_len, _ptr(out), _ptr(err),
-                                    _current_stream(stream)))
+    _done(_native().attention_q8(q, kv_pool, k_scale, v_scale, page_table, lens, block_size, max_len, out, err, stream))
 
 
 def nld_attention_shared_workspace_size(batch: int, m: int, n_q_heads: int) -> int:
@@ -440,22 +393,8 @@ def nld_attention_shared(q, kv_pool, shared_pages, shared_len: int, page_table, 
     """nld_attention for sequences that all start with the same shared_len keys, in the pages
     shared_pages [n] int32; page_table, lens and max_len count a sequence's own keys.  workspace: uint8
     of nld_attention_shared_workspace_size bytes (None with shared_len 0)."""
-    import torch
-    lib = load_library()
-    if q.dim() != 4 or kv_pool.dim() != 5 or page_table.dim() != 2:
-        raise ValueError("q [B, m, Hq, hd], kv_pool [n_pages, 2, Hkv, 64, hd] and page_table [B, pps] expected")
-    B, m, Hq, hd = q.shape
-    n_pages, Hkv, pps = kv_pool.shape[0], kv_pool.shape[2], page_table.shape[1]
-    n_shared = 0 if shared_pages is None else shared_pages.numel()
-    _check_tensors((("q", q, torch.bfloat16, None), ("kv_pool", kv_pool, torch.bfloat16, (n_pages, 2, Hkv, 64, hd)),
-                    ("shared_pages", shared_pages, torch.int32, (n_shared,)),
-                    ("page_table", page_table, torch.int32, (B, pps)), ("lens", lens, torch.int32, (B,)),
-                    ("out", out, torch.bfloat16, q.shape), ("workspace", workspace, torch.uint8, None),
-                    ("err", err, torch.int32, None)))
-    _done(lib, lib.nld_attention_shared(
-        _ptr(q), _ptr(kv_pool), _ptr(shared_pages), n_shared, shared_len, _ptr(page_table), pps, n_pages, _ptr(lens), B,
-        m, Hq, Hkv, hd, block_size, max_len, _ptr(out), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-        _ptr(err), _current_stream(stream)))
+    _done(_native().attention_shared(q, kv_pool, shared_pages, shared_len, page_table, lens, block_size, max_len, out,
+                                     workspace, err, stream))
 
 
 def nld_sample(logits, u, tokens_out, prob_out=None, temperature=None, top_k=None, top_p=None, min_p=None,
@@ -463,18 +402,4 @@ def nld_sample(logits, u, tokens_out, prob_out=None, temperature=None, top_k=Non
     """The next token of each row of logits [rows, vocab] (bf16 or fp32, rows evenly spaced) with the
     uniform numbers u [rows] fp32: tokens_out [rows] int32, prob_out [rows] fp32 (or None);
     temperature, top_p, min_p [rows] fp32 and top_k [rows] int32, each or None (off)."""
-    import torch
-    lib = load_library()
-    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("logits must be [rows, vocab], float32 or bfloat16")
-    rows, vocab = logits.shape
-    ld = logits.stride(0) if rows > 1 else vocab
-    if logits.get_device() != torch.cuda.current_device() or (vocab > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be on the current CUDA device, each row contiguous")
-    f, n = torch.float32, (rows,)
-    _check_tensors((("u", u, f, n), ("tokens_out", tokens_out, torch.int32, n), ("prob_out", prob_out, f, n),
-                    ("temperature", temperature, f, n), ("top_k", top_k, torch.int32, n), ("top_p", top_p, f, n),
-                    ("min_p", min_p, f, n)))
-    _done(lib, lib.nld_sample(_ptr(logits), NLD_F32 if logits.dtype == f else NLD_BF16, ld, rows, vocab, _ptr(u),
-                              _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(tokens_out), _ptr(prob_out),
-                              _current_stream(stream)))
+    _done(_native().sample(logits, u, tokens_out, prob_out, temperature, top_k, top_p, min_p, stream))
