@@ -2214,8 +2214,8 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
   if (!aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) || !aligned16(d_q_out) || !aligned16(d_kv_pool) ||
       !aligned16(d_rope) || !aligned16(d_q_gain) || !aligned16(d_k_gain))
     return fail(nullptr, NLD_ERR_ARG, "pointers must be 16-byte aligned");
-  // one thread per 16 bytes of half a head at most; the grid's x extent bounds them
-  if (static_cast<double>(batch) * m * (n_q_heads + 2.0 * n_kv_heads) * 16 > 2147483647.0 * 256)
+  // the kernel counts its warps (one per 8 heads of a token at least) in 32 bits
+  if (static_cast<double>(batch) * m * ((n_q_heads + 2.0 * n_kv_heads) / 8 + 1) > 2147483647.0)
     return fail(nullptr, NLD_ERR_ARG, "batch * m too large");
   QkvWriteArgs a{};
   a.q = d_q;
@@ -2245,7 +2245,7 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
   a.pps = pages_per_seq;
   a.n_pages = n_pages;
   a.err = d_err;
-  const cudaError_t e = launch_qkv_write(static_cast<cudaStream_t>(cuda_stream), a, dtype, kv_dtype, device_sms());
+  const cudaError_t e = launch_qkv_write(static_cast<cudaStream_t>(cuda_stream), a, dtype, kv_dtype);
   if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "cache write launch failed: %s", cudaGetErrorString(e));
   return NLD_OK;
 }

@@ -191,7 +191,7 @@ struct QkvWriteArgs {
   const float *k_scale, *v_scale;   // [Hkv] (e4m3)
   const int* page_table;
   int pps, n_pages;
-  int groups;                   // head groups of a token (set by the launcher)
+  int groups;                   // warps of a token (set by the launcher)
   int* err;
 };
 
@@ -239,7 +239,7 @@ cudaError_t launch_attention_simt(cudaStream_t st, const AttnArgs& a, int batch,
                                   int max_kv, bool pdl);
 
 cudaError_t init_shared_attention_attributes();
-cudaError_t launch_qkv_write(cudaStream_t st, QkvWriteArgs a, int dtype, int kv_dtype, int sms);
+cudaError_t launch_qkv_write(cudaStream_t st, const QkvWriteArgs& a, int dtype, int kv_dtype);
 void attn_q8_plan(int batch, int max_len, int sms, AttnQ8Args& a, int* mt);
 cudaError_t launch_attention_q8(cudaStream_t st, const AttnQ8Args& a, int batch, int mt);
 cudaError_t launch_sample(cudaStream_t st, const SampleArgs& a, int dtype, int sms);
