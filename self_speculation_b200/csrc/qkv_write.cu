@@ -11,8 +11,12 @@
 // heads of one token; a thread holds 16 bytes of the lower half of a head and the 16 bytes half a head
 // on, so a rotated pair never leaves its thread and the mean takes log2(lanes per head) shuffles.
 // All of a warp's q, k and v are requested before its position, page and angles, which wait on one
-// another (lens -> page table, lens -> angles).  Squares, norm and rotation are in fp32; the only
-// roundings are those to the output types.
+// another (lens -> page table, lens -> angles).  Squares, norm and rotation are in fp32, two numbers
+// an instruction; the only roundings are those to the output types.
+//
+// 3 blocks an SM (72 registers) and 4 heads a thread measured best: ragged prefill of 8 x 2048 rows of
+// 40 + 2 x 8 heads into an e4m3 cache 64 us, 2 blocks 75, 2 heads a thread 79 (4 blocks); chunks
+// staged through shared memory by cp.async, a persistent warp per token, 87.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -84,6 +88,32 @@ NLD_DEV void store_vec(__nv_fp8_storage_t* p, const float* x) {
 constexpr int kQkvThreads = 256;
 constexpr int kU = 4;   // heads of a thread
 
+// Two fp32 numbers worked on by one instruction.
+typedef unsigned long long f2;
+NLD_DEV f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+NLD_DEV void split(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+NLD_DEV f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+NLD_DEV f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+template <typename T>
+NLD_DEV void unpack2(const uint4& r, f2 (&x)[Vec<T>::n / 2]) {
+  float v[Vec<T>::n];
+  Vec<T>::unpack(r, v);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::n / 2; ++i) x[i] = pair(v[2 * i], v[2 * i + 1]);
+}
+
 // x / sc by its rounded reciprocal and one correction with the exact remainder (Markstein's method: the
 // rounded quotient); quotients that saturate, infinities and NaN stay as they are.
 NLD_DEV float divide(float x, float sc, float r) {
@@ -92,7 +122,7 @@ NLD_DEV float divide(float x, float sc, float r) {
 }
 
 template <typename T, typename C, int kHd>
-__global__ void __launch_bounds__(kQkvThreads) qkv_write_kernel(const QkvWriteArgs a) {
+__global__ void __launch_bounds__(kQkvThreads, 3) qkv_write_kernel(const QkvWriteArgs a) {
   constexpr int n = Vec<T>::n;
   constexpr int half = kHd / 2;
   constexpr int lanes = half / n;         // threads per head: 4, 8 or 16
@@ -123,15 +153,6 @@ __global__ void __launch_bounds__(kQkvThreads) qkv_write_kernel(const QkvWriteAr
     }
   }
   const bool norm = a.q_gain != nullptr;
-  uint4 gain[2][2];   // q, k
-  if (norm) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const T* g = static_cast<const T*>(j ? a.k_gain : a.q_gain) + lane * n;
-      gain[j][0] = __ldg(reinterpret_cast<const uint4*>(g));
-      gain[j][1] = __ldg(reinterpret_cast<const uint4*>(g + half));
-    }
-  }
   const long long s = static_cast<long long>(len) + i, p = s + a.position_offset;
   if (s < 0 || s >= static_cast<long long>(a.pps) * kPage || p < 0 || p >= a.rope_rows) {
     if (threadIdx.x % 32 == 0) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
@@ -139,14 +160,15 @@ __global__ void __launch_bounds__(kQkvThreads) qkv_write_kernel(const QkvWriteAr
   }
   const int slot = static_cast<int>(s);
   const int page = a.page_table[static_cast<size_t>(b) * a.pps + (slot >> 6)];
-  float2 cs[n];   // cos, sin
+  f2 cs[n / 2], sn[n / 2], ns[n / 2];   // cos, sin, -sin
   {
     const float4* t = reinterpret_cast<const float4*>(a.rope + static_cast<size_t>(p) * half + lane * n);
 #pragma unroll
     for (int e = 0; e < n / 2; ++e) {
       const float4 v = __ldg(t + e);
-      cs[2 * e] = make_float2(v.x, v.y);
-      cs[2 * e + 1] = make_float2(v.z, v.w);
+      cs[e] = pair(v.x, v.z);
+      sn[e] = pair(v.y, v.w);
+      ns[e] = pair(-v.y, -v.w);
     }
   }
   if (page < 0 || page >= a.n_pages) {
@@ -157,36 +179,44 @@ __global__ void __launch_bounds__(kQkvThreads) qkv_write_kernel(const QkvWriteAr
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
     const int h = h0 + u * kHeads;
-    float x[n], y[n];
-    Vec<T>::unpack(lo[u], x);
-    Vec<T>::unpack(hi[u], y);
+    f2 x2[n / 2], y2[n / 2];
+    unpack2<T>(lo[u], x2);
+    unpack2<T>(hi[u], y2);
     if (norm) {
-      float ss = 0.f;
+      f2 s2 = mul2(x2[0], x2[0]);
 #pragma unroll
-      for (int e = 0; e < n; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
+      for (int e = 1; e < n / 2; ++e) s2 = fma2(x2[e], x2[e], s2);
+#pragma unroll
+      for (int e = 0; e < n / 2; ++e) s2 = fma2(y2[e], y2[e], s2);
+      float ss, s1;
+      split(s2, ss, s1);
+      ss += s1;
 #pragma unroll
       for (int off = lanes >> 1; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
       if (h < a.Hq + a.Hkv) {
         const float inv = rsqrtf(fmaf(ss, 1.0f / kHd, a.eps));
-        const bool is_k = h >= a.Hq;
-        float gx[n], gy[n];
-        Vec<T>::unpack(is_k ? gain[1][0] : gain[0][0], gx);
-        Vec<T>::unpack(is_k ? gain[1][1] : gain[0][1], gy);
+        const f2 inv2 = pair(inv, inv);
+        const T* g = static_cast<const T*>(h < a.Hq ? a.q_gain : a.k_gain) + lane * n;
+        f2 g2[n / 2];
+        unpack2<T>(__ldg(reinterpret_cast<const uint4*>(g)), g2);
 #pragma unroll
-        for (int e = 0; e < n; ++e) {
-          x[e] = x[e] * inv * gx[e];
-          y[e] = y[e] * inv * gy[e];
-        }
+        for (int e = 0; e < n / 2; ++e) x2[e] = mul2(mul2(x2[e], inv2), g2[e]);
+        unpack2<T>(__ldg(reinterpret_cast<const uint4*>(g + half)), g2);
+#pragma unroll
+        for (int e = 0; e < n / 2; ++e) y2[e] = mul2(mul2(y2[e], inv2), g2[e]);
       }
     }
     if (h >= heads) continue;
-    if (h < a.Hq + a.Hkv) {
+    float x[n], y[n];
 #pragma unroll
-      for (int e = 0; e < n; ++e) {
-        const float c = x[e], r = y[e];
-        x[e] = c * cs[e].x - r * cs[e].y;
-        y[e] = r * cs[e].x + c * cs[e].y;
+    for (int e = 0; e < n / 2; ++e) {
+      f2 ox = x2[e], oy = y2[e];
+      if (h < a.Hq + a.Hkv) {
+        ox = fma2(x2[e], cs[e], mul2(y2[e], ns[e]));
+        oy = fma2(y2[e], cs[e], mul2(x2[e], sn[e]));
       }
+      split(ox, x[2 * e], x[2 * e + 1]);
+      split(oy, y[2 * e], y[2 * e + 1]);
     }
     if (h < a.Hq) {
       T* dst = static_cast<T*>(a.q_out) + (static_cast<size_t>(tok) * a.Hq + h) * kHd;
