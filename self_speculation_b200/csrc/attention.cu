@@ -22,6 +22,7 @@
 // distributed shared memory, in split order.  No global scratch, no atomics.
 #include <atomic>
 
+#include "attn_share.cuh"
 #include "common.cuh"
 
 namespace nld {
@@ -120,26 +121,6 @@ NLD_DEV void tmem_ld_wait_regs(uint32_t (&r)[16]) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
                  "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
                  "+r"(r[14]), "+r"(r[15])::"memory");
-}
-
-// The shared-prefix attention's part of a row's merge: the merged (O, max, sum) of row `prow` (token x
-// query head), dims 4 d4 ..  The prefix pass leaves it in global memory (true: done with the
-// row); the own pass takes the prefix pass's in.
-template <int kShare>
-NLD_DEV bool share_merge(const AttnArgs& a, size_t prow, int d4, float M, float& L, float4& acc) {
-  if constexpr (kShare == kPrefixPass) {
-    reinterpret_cast<float4*>(a.part_o)[prow * 32 + d4] = acc;
-    if (d4 == 0) a.part_ml[prow] = make_float2(M, L);
-    return true;
-  }
-  if (a.part_o == nullptr) return false;   // no prefix
-  const float2 ml = a.part_ml[prow];
-  const float4 o = reinterpret_cast<const float4*>(a.part_o)[prow * 32 + d4];
-  const float top = fmaxf(M, ml.x);
-  const float w = M == -INFINITY ? 0.f : exp2f(M - top), v = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-  L = w * L + v * ml.y;
-  acc = make_float4(w * acc.x + v * o.x, w * acc.y + v * o.y, w * acc.z + v * o.z, w * acc.w + v * o.w);
-  return false;
 }
 
 }  // namespace
@@ -572,7 +553,7 @@ __global__ void __launch_bounds__(32 * kMaxW, 1)
     }
     if constexpr (kShare != 0) {
       const size_t prow = (static_cast<size_t>(b) * a.m + p0 + p) * a.Hq + static_cast<size_t>(g * a.G + (r - p * a.G));
-      if (share_merge<kShare>(a, prow, d4, M, L, acc)) continue;
+      if (share_merge<kShare>(a.part_o, a.part_ml, prow, d4, M, L, acc)) continue;
     }
     const float inv = (L > 0.f) ? 1.f / L : 0.f;
     store2(r, d4 * 4, acc.x * inv, acc.y * inv);
@@ -1201,7 +1182,7 @@ __global__ void __launch_bounds__(tc_threads(kRT), 1)
     if constexpr (kShare != 0) {
       const int p = rr / a.G;
       const size_t prow = (static_cast<size_t>(b) * a.m + p0 + p) * a.Hq + static_cast<size_t>(g * a.G + (rr - p * a.G));
-      if (share_merge<kShare>(a, prow, d4, M, L, acc)) continue;
+      if (share_merge<kShare>(a.part_o, a.part_ml, prow, d4, M, L, acc)) continue;
     }
     const float inv = (L > 0.f) ? 1.f / L : 0.f;
     if (e == tid) stamp(14);

@@ -2278,13 +2278,12 @@ nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float*
   TRY(attn_check(d_q, d_kv_pool, d_page_table, pages_per_seq, n_pages, d_lens, batch, m, n_q_heads, n_kv_heads,
                  head_dim, block_size, max_len, d_out));
   if (!d_k_scale || !d_v_scale) return fail(nullptr, NLD_ERR_ARG, "NULL scale pointer");
-  AttnQ8Args a{};
+  AttnSmallArgs a{};
   a.m = m;
   a.Hq = n_q_heads;
   a.Hkv = n_kv_heads;
   a.G = n_q_heads / n_kv_heads;
-  int mt = 1;
-  attn_q8_plan(batch, max_len, device_sms(), a, &mt);
+  attn_small_plan(batch, max_len, device_sms(), a);
   if (static_cast<long long>(batch) * a.r_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
   a.q = d_q;
   a.out = d_out;
@@ -2298,7 +2297,7 @@ nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float*
   a.block_size = block_size;
   a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
   a.err = d_err;
-  const cudaError_t e = launch_attention_q8(static_cast<cudaStream_t>(cuda_stream), a, batch, mt);
+  const cudaError_t e = launch_attention_small(static_cast<cudaStream_t>(cuda_stream), a, batch, false);
   if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
   return NLD_OK;
 }
@@ -2321,53 +2320,90 @@ nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const in
   const size_t need = nld_attention_shared_workspace_size(batch, m, n_q_heads);
   if (shared_len > 0 && (!d_workspace || workspace_bytes < need || !aligned16(d_workspace)))
     return fail(nullptr, NLD_ERR_ARG, "workspace must be 16-byte aligned and at least %zu bytes", need);
-  const cudaError_t ae = init_shared_attention_attributes();
-  if (ae != cudaSuccess) {
-    cudaGetLastError();
-    return fail(nullptr, NLD_ERR_CUDA, "setting kernel shared-memory limits failed: %s", cudaGetErrorString(ae));
-  }
-  CUtensorMap map;
-  if (!make_map_bf16(&map, d_kv_pool, 128, static_cast<uint64_t>(n_pages) * 2 * n_kv_heads * kPage, kPage))
-    return fail(nullptr, NLD_ERR_CUDA, "tensor map encode failed (pool)");
   const int sms = device_sms();
-  const AttnCapacity cap = [](int S, int NW, int stages, int tc) { return attn_device_capacity(false, S, NW, stages, tc); };
-  AttnArgs a{};
-  a.q = d_q;
-  a.out = d_out;
-  a.out_ld = static_cast<size_t>(n_q_heads) * 128;
-  a.Hq = n_q_heads;
-  a.Hkv = n_kv_heads;
-  a.hd = 128;
-  a.block_size = block_size;
-  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
-  a.err = d_err;
+  const int G = n_q_heads / n_kv_heads;
+  const float scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
+  float* part_o = nullptr;   // rows of 512 bytes, then the (max, sum) pairs
+  float2* part_ml = nullptr;
   if (shared_len > 0) {
-    a.part_o = static_cast<float*>(d_workspace);   // rows of 512 bytes, then the (max, sum) pairs
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(batch) * m * n_q_heads * 128);
+    part_o = static_cast<float*>(d_workspace);
+    part_ml = reinterpret_cast<float2*>(part_o + static_cast<size_t>(batch) * m * n_q_heads * 128);
   }
-  AttnArgs own = a, pre = a;
-  own.share = kOwnPass;
-  own.m = m;
-  own.lens = d_lens;
-  own.page_table = d_page_table;
-  own.pps = pages_per_seq;
-  attn_plan(batch, m, n_q_heads, n_kv_heads, max_len, sms, own, cap, 0, 0, g_attn_kernel.load(), g_attn_tile.load(), false);
-  pre.share = kPrefixPass;
-  pre.m = batch * m;
-  pre.key_end = shared_len;
-  pre.page_table = d_shared_pages;
-  pre.pps = (shared_len + kPage - 1) / kPage;
-  attn_plan(1, pre.m, n_q_heads, n_kv_heads, std::max(1, shared_len), sms, pre, cap, 0, 0, g_attn_kernel.load(),
-            g_attn_tile.load(), false);
-  if (static_cast<long long>(batch) * own.q_tiles > 65535 || pre.q_tiles > 65535)
-    return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
-  cudaError_t e = cudaSuccess;
-  if (shared_len > 0) e = launch_attention_mma(static_cast<cudaStream_t>(cuda_stream), &map, pre, 1, false);
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  CUtensorMap map;
+  bool have_map = false;
+  // One pass: rows of `seqs` sequences of `rows` positions each, over max_len keys at most.  Up to
+  // kSmallRows rows of a kv head take the kernel for small query tiles, more the planner's choice.
+  constexpr int kSmallRows = 64;
+  auto pass = [&](int share, int seqs, int rows, const int32_t* table, int pps, int max_keys, bool pdl, bool launch) -> nld_status {
+    cudaError_t e = cudaSuccess;
+    if (g_attn_kernel.load() == 0 && static_cast<long long>(rows) * G <= kSmallRows) {
+      AttnSmallArgs a{};
+      a.q = d_q;
+      a.out = d_out;
+      a.pool = d_kv_pool;
+      a.lens = d_lens;
+      a.page_table = table;
+      a.pps = pps;
+      a.n_pages = n_pages;
+      a.m = rows;
+      a.Hq = n_q_heads;
+      a.Hkv = n_kv_heads;
+      a.G = G;
+      a.block_size = block_size;
+      a.scale_log2 = scale_log2;
+      a.share = share;
+      a.key_end = shared_len;
+      a.part_o = part_o;
+      a.part_ml = part_ml;
+      a.err = d_err;
+      attn_small_plan(seqs, max_keys, sms, a);
+      if (static_cast<long long>(seqs) * a.r_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
+      if (launch) e = launch_attention_small(st, a, seqs, pdl);
+    } else {
+      if (!have_map) {
+        if ((e = init_shared_attention_attributes()) != cudaSuccess) {
+          cudaGetLastError();
+          return fail(nullptr, NLD_ERR_CUDA, "setting kernel shared-memory limits failed: %s", cudaGetErrorString(e));
+        }
+        if (!make_map_bf16(&map, d_kv_pool, 128, static_cast<uint64_t>(n_pages) * 2 * n_kv_heads * kPage, kPage))
+          return fail(nullptr, NLD_ERR_CUDA, "tensor map encode failed (pool)");
+        have_map = true;
+      }
+      AttnArgs a{};
+      a.q = d_q;
+      a.out = d_out;
+      a.out_ld = static_cast<size_t>(n_q_heads) * 128;
+      a.m = rows;
+      a.Hq = n_q_heads;
+      a.Hkv = n_kv_heads;
+      a.hd = 128;
+      a.lens = d_lens;
+      a.page_table = table;
+      a.pps = pps;
+      a.block_size = block_size;
+      a.scale_log2 = scale_log2;
+      a.share = share;
+      a.key_end = shared_len;
+      a.part_o = part_o;
+      a.part_ml = part_ml;
+      a.err = d_err;
+      attn_plan(seqs, rows, n_q_heads, n_kv_heads, max_keys, sms, a,
+                [](int S, int NW, int stages, int tc) { return attn_device_capacity(false, S, NW, stages, tc); }, 0, 0,
+                g_attn_kernel.load(), g_attn_tile.load(), false);
+      if (static_cast<long long>(seqs) * a.q_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
+      if (launch) e = launch_attention_mma(st, &map, a, seqs, pdl);
+    }
+    if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
+    return NLD_OK;
+  };
+  auto own = [&](bool launch) { return pass(kOwnPass, batch, m, d_page_table, pages_per_seq, max_len, shared_len > 0, launch); };
+  if (shared_len > 0) {
+    TRY(own(false));   // refused before the prefix pass is launched, if at all
+    TRY(pass(kPrefixPass, 1, batch * m, d_shared_pages, (shared_len + kPage - 1) / kPage, shared_len, false, true));
+  }
   // the own pass may start beside the prefix pass: it waits for it before its merge
-  if (e == cudaSuccess)
-    e = launch_attention_mma(static_cast<cudaStream_t>(cuda_stream), &map, own, batch, shared_len > 0);
-  if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
-  return NLD_OK;
+  return own(true);
 }
 
 nld_status nld_sample(const void* d_logits, int dtype, long long ld, int rows, int vocab, const float* d_u,

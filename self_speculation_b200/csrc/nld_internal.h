@@ -195,18 +195,23 @@ struct QkvWriteArgs {
   int* err;
 };
 
-// Attention over the e4m3 cache (nld_attention_q8).
-struct AttnQ8Args {
+// Attention for small query tiles: over the e4m3 cache (nld_attention_q8), or a pass of the
+// shared-prefix attention over the bf16 cache.
+struct AttnSmallArgs {
   const void* q;                // [batch, m, Hq, 128] bf16
   void* out;
-  const void* pool;             // [n_pages][2][Hkv][64][128] e4m3
-  const float *k_scale, *v_scale;   // [Hkv]
-  const int* lens;
+  const void* pool;             // [n_pages][2][Hkv][64][128] e4m3 or bf16
+  const float *k_scale, *v_scale;   // [Hkv] (e4m3)
+  const int* lens;              // (not the prefix pass)
   const int* page_table;
   int pps, n_pages;
   int m, Hq, Hkv, G, block_size;
-  int r_tiles, S;               // tiles of query rows, KV splits (cluster size)
+  int mt, r_tiles, S;           // 16-row tiles of a CTA, tiles of query rows, KV splits (cluster size)
   float scale_log2;             // log2(e) / sqrt(hd)
+  int share;                    // 0: e4m3; kOwnPass or kPrefixPass: bf16
+  int key_end;                  // prefix pass: keys of the prefix
+  float* part_o;                // as in AttnArgs
+  float2* part_ml;
   int* err;
 };
 
@@ -240,8 +245,8 @@ cudaError_t launch_attention_simt(cudaStream_t st, const AttnArgs& a, int batch,
 
 cudaError_t init_shared_attention_attributes();
 cudaError_t launch_qkv_write(cudaStream_t st, const QkvWriteArgs& a, int dtype, int kv_dtype);
-void attn_q8_plan(int batch, int max_len, int sms, AttnQ8Args& a, int* mt);
-cudaError_t launch_attention_q8(cudaStream_t st, const AttnQ8Args& a, int batch, int mt);
+void attn_small_plan(int batch, int max_len, int sms, AttnSmallArgs& a);
+cudaError_t launch_attention_small(cudaStream_t st, const AttnSmallArgs& a, int batch, bool pdl);
 cudaError_t launch_sample(cudaStream_t st, const SampleArgs& a, int dtype, int sms);
 
 struct EmbedArgs {
