@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libnld.so")
 OPERATORS = os.path.join(PKG, "_operators.so")
 SOURCES = ["nld_api.cu", "gemm_tc.cu", "gemm_simt.cu", "attention.cu", "decode_kernels.cu",
-           "attention_small.cu", "qkv_write.cu", "sampling.cu"]
+           "attention_small.cu", "attention_wide.cu", "qkv_write.cu", "sampling.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

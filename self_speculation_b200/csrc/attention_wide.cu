@@ -1,0 +1,726 @@
+// Block-causal GQA attention over the paged KV cache for wide query tiles (up to 128 rows of a kv head),
+// on tcgen05: over the e4m3 cache (nld_attention_q8) and, for both passes of the shared-prefix attention
+// (nld_attention_shared), over the bf16 cache.
+//
+//   o = softmax(q K^T / sqrt(hd) + mask) V;   e4m3: K = k_scale[g] k8,  V = v_scale[g] v8
+//
+// One CTA per (KV split, kv head, sequence x query tile); row = position * G + head.  A tile of 128 keys
+// costs 1024 cycles of tensor core (S = Q K^T and O += P V, 128 x 128 x 128 each) and as many of the exponential
+// unit (16 a cycle and SM), so the two have to run side by side: the even and the odd key tiles are two
+// streams, each with its own S, O, running max and sum, its own four softmax warps (a thread per row) and its
+// own issuing thread.  While one stream's softmax runs, the other's products do.  Tensor memory is full: S of
+// both streams (P is written over S, in 16 bits), O of both.  The streams' partials meet in shared memory at
+// the end, those of the KV splits over the cluster's distributed shared memory, in a fixed order.
+//
+// bf16: K and V come by TMA into rings of three tiles.  e4m3: a page's K (or V) rows of a kv head are 8 KB in a
+// row and come by bulk copies; four warps turn them into fp16 tiles (exact), two of K and two of V, in the
+// swizzled layout of the descriptors.  K's place frees when S is done, V's when O is.  Q's rows are scaled by a power
+// of two into fp16's range there, and P is rounded to fp16 (attention_small.cu has the errors); over the bf16
+// cache P is rounded to bf16.  The maximum that exponents refer to moves only when it has grown by 2^8, so O is
+// rarely rescaled; sums, maxima and O are in fp32.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "attn_share.cuh"
+#include "common.cuh"
+
+namespace nld {
+
+namespace {
+
+constexpr int kTile = 128;                   // keys of a tile
+constexpr int kTileBytes = kTile * 256;      // K (or V) of a tile in 16 bits: [2 boxes of 64 dims][128 keys][128 B]
+constexpr int kBoxBytes = kTileBytes / 2;
+constexpr int kRawBytes = kTile * 128;       // the same in e4m3: [128 keys][128 B]
+constexpr int kQBytes = 128 * 256;           // [2 boxes][128 rows][128 B]
+constexpr int kSoftmax = 256;                // threads: two streams of 128
+constexpr float kMove = 8.f;                 // log2 units
+constexpr uint64_t kWait = 2000000000ull;
+
+template <typename E>
+struct Wide {   // bf16
+  static constexpr bool kQ8 = false;
+  static constexpr int kK = 3, kV = 3, kRaw = 0;        // tiles of K, of V, raw ones
+  static constexpr int kThreads = kSoftmax + 96;        // two issuing warps, a loading one
+};
+template <>
+struct Wide<__nv_fp8_storage_t> {
+  static constexpr bool kQ8 = true;
+  static constexpr int kK = 2, kV = 2, kRaw = 2;
+  static constexpr int kThreads = kSoftmax + 96 + 128;   // and four converting ones
+};
+template <typename E>
+__host__ __device__ constexpr int wide_bytes() {
+  return 1024 + kQBytes + (Wide<E>::kK + Wide<E>::kV) * kTileBytes + Wide<E>::kRaw * 2 * kRawBytes + 512;
+}
+
+NLD_DEV void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Descriptor of an MN-major operand in 128-byte-swizzled atoms (64 elements of MN x 8 of K): `lbo` bytes
+// between 64-element MN blocks, `sbo` between groups of 8 K rows.
+NLD_DEV uint64_t desc_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
+}
+NLD_DEV void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Wait for this thread's loads of tensor memory; the registers are operands so that no use moves ahead of it.
+NLD_DEV void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+NLD_DEV void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
+      "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+NLD_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+NLD_DEV float exp2_hw(float x) {   // relative error about 2^-22; 2^-inf = 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool kHalf>
+NLD_DEV uint32_t pack16(float lo, float hi) {
+  if constexpr (kHalf) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+// Four e4m3 values as two fp16 pairs: exact.
+NLD_DEV void halves_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+NLD_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+template <typename E, int kShare>
+__global__ void __launch_bounds__(Wide<E>::kThreads, 1)
+    attn_wide_kernel(const __grid_constant__ CUtensorMap tmKV, const AttnWideArgs a) {
+  using W = Wide<E>;
+  constexpr bool kQ8 = W::kQ8;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + kQBytes;                  // [kK] tiles
+  uint8_t* sV = sK + W::kK * kTileBytes;       // [kV]
+  uint8_t* sRaw = sV + W::kV * kTileBytes;     // [kRaw][K, V]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sRaw + W::kRaw * 2 * kRawBytes);
+  uint64_t* k_full = bars;             // [kK] tile of K there
+  uint64_t* k_empty = bars + 3;        // [kK] S of the tile done
+  uint64_t* v_full = bars + 6;         // [kV]
+  uint64_t* v_empty = bars + 9;        // [kV] O += P V of the tile done
+  uint64_t* raw_full = bars + 12;      // [kRaw] bytes landed
+  uint64_t* raw_empty = bars + 14;     // [kRaw] converted
+  uint64_t* s_full = bars + 16;        // [2] by stream: S written
+  uint64_t* p_full = bars + 18;        // [2] P written, S read
+  uint64_t* pv_done = bars + 20;       // [2] O += P V done
+  uint64_t* fin = bars + 22;           // every product done
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 23);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(bars + 24);
+  int* s_bad = reinterpret_cast<int*>(bars + 25);   // [kRaw][2] the page is outside the pool
+
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int split = blockIdx.x, g = blockIdx.y;
+  const int b = blockIdx.z / a.q_tiles, qt = blockIdx.z - b * a.q_tiles;
+  const int all = a.m * a.G;                              // rows of the (sequence, kv head)
+  const int r0 = qt * a.rows, rows = min(a.rows, all - r0);   // of this CTA
+  const bool softmax_thr = tid < kSoftmax;
+  const bool issue_thr = tid == kSoftmax || tid == kSoftmax + 32;
+  const bool load_thr = tid == kSoftmax + 64;
+
+  if (tid == 0) {
+    for (int i = 0; i < W::kK; ++i) {
+      mbar_init(&k_full[i], kQ8 ? 4 : 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < W::kV; ++i) {
+      mbar_init(&v_full[i], kQ8 ? 4 : 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < W::kRaw; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(fin, 2);
+    *s_abort = 0;
+    fence_mbar_init();
+    if constexpr (!kQ8) tma_prefetch_desc(&tmKV);
+  }
+  if (warp == kSoftmax / 32) {
+    tmem_alloc(s_tmem, 512);   // S of the streams, O of the streams
+    tmem_relinquish();
+  }
+
+  int len = 0;
+  if constexpr (kShare != kPrefixPass) {
+    len = a.lens[b];
+    if (len < 0 || len > a.pps * kPage - a.m) {   // keys stay inside the page table row
+      if (tid == 0) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
+      len = max(0, min(len, a.pps * kPage - a.m));
+    }
+  }
+  // keys that a row sees: [0, seen)
+  auto seen_by = [&](int r) {
+    if constexpr (kShare == kPrefixPass) return a.key_end;
+    return len + min((r / a.G) / a.block_size * a.block_size + a.block_size, a.m);
+  };
+  const int kv_end = seen_by(r0 + rows - 1);   // the last row sees the most
+  const int n_pages = (kv_end + kPage - 1) / kPage;
+  const int n_tiles = (kv_end + kTile - 1) / kTile;
+  const int per = (n_tiles + a.S - 1) / a.S;
+  const int t_lo = split * per;
+  const int ntile = max(0, min(n_tiles, t_lo + per) - t_lo);
+
+  // Q into shared memory, K-major in 128-byte-swizzled boxes: thread (stream x, row r) writes box x of row r
+  const int x = tid >> 7, r = tid & 127;   // softmax threads
+  float c = a.scale_log2;                  // the scores' scale to log2 units
+  if (softmax_thr) {
+    const int row = r0 + r, pos = row / a.G;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        static_cast<const __nv_bfloat16*>(a.q) +
+        ((static_cast<size_t>(b) * a.m + (r < rows ? pos : 0)) * a.Hq + static_cast<size_t>(g) * a.G + (r < rows ? row - pos * a.G : 0)) * 128);
+    float down = 1.f;
+    if constexpr (kQ8) {
+      float big = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const uint4 v = src[i];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+      }
+      // 2^-e brings the largest element into [1, 2); zero, subnormal and infinite rows keep e in range
+      const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -126), 126);
+      const float ks = a.k_scale[g];
+      down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), ks);   // (the scores' scale stays positive)
+      c = fabsf(ks) * a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        v = src[8 * x + i];
+        if constexpr (kQ8) {
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack16<true>(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xffff0000u) * down);
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      *reinterpret_cast<uint4*>(sQ + x * (kQBytes / 2) + r * 128 + ((i ^ (r & 7)) << 4)) = v;
+    }
+    fence_proxy_async();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  if constexpr (kShare == kPrefixPass) pdl_launch_dependents();
+
+  bool aborted = false;
+  float m_ref = -INFINITY, l_sum = 0.f;
+  int n_issued = 0;   // tiles requested (load_thr)
+  const int* table = a.page_table + static_cast<size_t>(b) * a.pps;
+  if (load_thr) {
+    // ---------------------------------------------------------------- loads --
+    for (int j = 0; j < ntile; ++j) {
+      int page[2];
+      bool bad[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int p = 2 * (t_lo + j) + h;   // a page past the keys: the first page again, its keys masked
+        page[h] = table[p < n_pages ? p : p - 1];
+        bad[h] = page[h] < 0 || page[h] >= a.n_pages;
+        if (bad[h]) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
+      }
+      if constexpr (kQ8) {
+        const int st = j % 2;
+        if (j >= 2 && (*s_abort || !mbar_wait(&raw_empty[st], static_cast<uint32_t>(j / 2 - 1) & 1u, kWait))) {
+          aborted = true;
+          break;
+        }
+        ++n_issued;
+        s_bad[st * 2] = bad[0];
+        s_bad[st * 2 + 1] = bad[1];
+        mbar_arrive_expect_tx(&raw_full[st], 2 * kRawBytes);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* kp = static_cast<const uint8_t*>(a.pool) +
+                              (static_cast<size_t>(bad[h] ? 0 : page[h]) * 2 * a.Hkv + g) * (kPage * 128);
+          bulk_load(sRaw + (st * 2) * kRawBytes + h * (kRawBytes / 2), kp, kRawBytes / 2, &raw_full[st]);
+          bulk_load(sRaw + (st * 2 + 1) * kRawBytes + h * (kRawBytes / 2), kp + static_cast<size_t>(a.Hkv) * (kPage * 128),
+                    kRawBytes / 2, &raw_full[st]);
+        }
+      } else {
+        const int st = j % 3;
+        if (j >= 3 && (*s_abort || !mbar_wait(&k_empty[st], static_cast<uint32_t>(j / 3 - 1) & 1u, kWait))) {
+          aborted = true;
+          break;
+        }
+        // (a page outside the pool: rows outside the tensor, which read as zeros)
+        mbar_arrive_expect_tx(&k_full[st], kTileBytes);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int box = 0; box < 2; ++box)
+            tma_load_2d(sK + st * kTileBytes + box * kBoxBytes + h * (kPage * 128), &tmKV, &k_full[st], box * 64,
+                        bad[h] ? -kPage : (page[h] * 2 * a.Hkv + g) * kPage);
+        if (j >= 3 && (*s_abort || !mbar_wait(&v_empty[st], static_cast<uint32_t>(j / 3 - 1) & 1u, kWait))) {
+          mbar_wait(&k_full[st], static_cast<uint32_t>(j / 3) & 1u, kWait);   // the copies in flight land
+          aborted = true;
+          break;
+        }
+        ++n_issued;
+        mbar_arrive_expect_tx(&v_full[st], kTileBytes);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int box = 0; box < 2; ++box)
+            tma_load_2d(sV + st * kTileBytes + box * kBoxBytes + h * (kPage * 128), &tmKV, &v_full[st], box * 64,
+                        bad[h] ? -kPage : ((page[h] * 2 + 1) * a.Hkv + g) * kPage);
+      }
+    }
+    if (aborted) {
+      *s_abort = 1;
+      set_err(a.err, NLD_DEVERR_TIMEOUT);
+    }
+  } else if (issue_thr) {
+    // ------------------------------------------- products of stream y: tiles y, y + 2, .. --
+    const int y = tid == kSoftmax ? 0 : 1;
+    constexpr uint32_t kF16 = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);   // fp32 accumulator, 128 x 128, fp16
+    constexpr uint32_t idS = kQ8 ? kF16 : idesc_bf16_f32(128, 128);
+    constexpr uint32_t idO = idS | (1u << 16);   // B (V) MN-major
+    const uint32_t s_col = tmem + y * 128, o_col = tmem + 256 + y * 128;
+    for (int j = y, i = 0; j < ntile; j += 2, ++i) {
+      const int ks = j % W::kK, vs = j % W::kV;
+      // S over the P of the stream's tile before, once O += P V has read it
+      if (*s_abort || !mbar_wait(&k_full[ks], static_cast<uint32_t>(j / W::kK) & 1u, kWait) ||
+          (i > 0 && !mbar_wait(&pv_done[y], static_cast<uint32_t>(i - 1) & 1u, kWait))) {
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int box = 0; box < 2; ++box)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_f16(s_col, sdesc_k_sw128(smem_u32(sQ + box * (kQBytes / 2))) + 2 * kk,
+                     sdesc_k_sw128(smem_u32(sK + ks * kTileBytes + box * kBoxBytes)) + 2 * kk, idS, (box > 0 || kk > 0) ? 1u : 0u);
+      tc_commit(&k_empty[ks]);
+      tc_commit(&s_full[y]);
+      if (!mbar_wait(&p_full[y], static_cast<uint32_t>(i) & 1u, kWait) || *s_abort ||
+          !mbar_wait(&v_full[vs], static_cast<uint32_t>(j / W::kV) & 1u, kWait)) {
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)   // 16 keys: 8 columns of P
+        tc_mma_ts(o_col, s_col + k * 8, desc_mn(smem_u32(sV + vs * kTileBytes + k * 2048), kBoxBytes, 1024), idO,
+                  (i > 0 || k > 0) ? 1u : 0u);
+      tc_commit(&v_empty[vs]);
+      tc_commit(&pv_done[y]);
+    }
+    if (aborted) {
+      *s_abort = 1;
+      set_err(a.err, NLD_DEVERR_TIMEOUT);
+    }
+    // every product of this thread is done before tensor memory is released
+    tc_commit(fin);
+    mbar_wait(fin, 0, kWait);
+  } else if (softmax_thr) {
+    // ----------------------------------------------------------- softmax of stream x, row r --
+    const int seen = r < rows ? seen_by(r0 + r) : 0;
+    const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lane + x * 128, o_at = tmem + lane + 256 + x * 128;
+    for (int j = x, i = 0; j < ntile; j += 2, ++i) {
+      // tcgen05.ld / st are for whole warps: every exit of this loop is taken by the warp together
+      if (!__all_sync(0xffffffffu, !*s_abort && mbar_wait(&s_full[x], static_cast<uint32_t>(i) & 1u, kWait))) {
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+      const int left = seen - (t_lo + j) * kTile;   // keys of the tile that the row sees
+      const bool whole = __all_sync(0xffffffffu, left >= kTile);
+      uint32_t s[2][32];
+      float mx = -INFINITY;
+      tmem_ld32_nowait(s_at, s[0]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        tmem_wait_ld(s[u & 1]);
+        if (u < 3) tmem_ld32_nowait(s_at + (u + 1) * 32, s[(u + 1) & 1]);
+        float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (whole) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(s[u & 1][k]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], u * 32 + k < left ? __uint_as_float(s[u & 1][k]) : -INFINITY);
+        }
+        mx = fmaxf(mx, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
+      }
+      tmem_ld32_nowait(s_at, s[0]);   // once more for the exponents
+      mx *= c;
+      const bool move = mx > m_ref + kMove;
+      const bool scale_o = move && m_ref != -INFINITY;
+      if (__any_sync(0xffffffffu, scale_o)) {   // (i > 0: m_ref was set)
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(i - 1) & 1u, kWait))) {
+          tmem_wait_ld(s[0]);
+          aborted = true;
+          break;
+        }
+        tc_fence_after();
+        tmem_wait_ld(s[0]);
+        const float alpha = scale_o ? exp2f(m_ref - mx) : 1.f;
+#pragma unroll 1
+        for (int u = 0; u < 8; ++u) {
+          float o[16];
+          uint32_t w[16];
+          tmem_ld16(o_at + u * 16, o);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * alpha);
+          tmem_st16u(o_at + u * 16, w);
+        }
+        tmem_wait_st();
+        l_sum *= alpha;
+      }
+      if (move) m_ref = mx;
+      const float nb = m_ref == -INFINITY ? 0.f : -m_ref;
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        tmem_wait_ld(s[u & 1]);
+        if (u < 3) tmem_ld32_nowait(s_at + (u + 1) * 32, s[(u + 1) & 1]);
+        uint32_t p[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float e0 = fmaf(__uint_as_float(s[u & 1][2 * k]), c, nb), e1 = fmaf(__uint_as_float(s[u & 1][2 * k + 1]), c, nb);
+          if (!whole) {
+            e0 = u * 32 + 2 * k < left ? e0 : -INFINITY;
+            e1 = u * 32 + 2 * k + 1 < left ? e1 : -INFINITY;
+          }
+          const float p0 = exp2_hw(e0), p1 = exp2_hw(e1);
+          ls[k & 3] += p0 + p1;
+          p[k] = pack16<kQ8>(p0, p1);
+        }
+        tmem_st16u(s_at + u * 16, p);   // P of keys 32 u .. over scores read before
+      }
+      l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      tmem_wait_st();
+      if constexpr (!kQ8) {
+        // V rows behind the last key: P is 0 there, V may be anything
+        const int dead = (t_lo + j + 1) * kTile - kv_end;
+        if (dead > 0) {
+          const int vs = j % W::kV;
+          if (!__all_sync(0xffffffffu, mbar_wait(&v_full[vs], static_cast<uint32_t>(j / W::kV) & 1u, kWait))) {
+            aborted = true;
+            break;
+          }
+          uint8_t* v = sV + vs * kTileBytes + (kTile - dead) * 128;
+          for (int e = r; e < dead * 16; e += 128)
+            *reinterpret_cast<uint4*>(v + (e & 1) * kBoxBytes + (e >> 1) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if ((tid & 31) == 0) mbar_arrive(&p_full[x]);
+    }
+    const int mine = ntile > x ? (ntile - x + 1) / 2 : 0;   // tiles of the stream
+    if (!aborted && mine > 0 &&
+        !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(mine - 1) & 1u, kWait)))
+      aborted = true;
+    if (aborted) {
+      *s_abort = 1;
+      set_err(a.err, NLD_DEVERR_TIMEOUT);
+    }
+    tc_fence_after();
+  } else if constexpr (kQ8) {
+    if (tid >= kSoftmax + 96) {
+      // ------------------------------------------------------------- e4m3 to fp16 --
+      const int ct = tid - (kSoftmax + 96), row_of = ct >> 3, ch = ct & 7;   // 16 rows at a time, 16 bytes of one
+      for (int j = 0; j < ntile && !aborted; ++j) {
+        const int st = j % 2;
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {   // K, then V
+          uint64_t* empty = v ? v_empty : k_empty;
+          const bool ok = !*s_abort && mbar_wait(&raw_full[st], static_cast<uint32_t>(j / 2) & 1u, kWait) &&
+                          (j < 2 || mbar_wait(&empty[st], static_cast<uint32_t>(j / 2 - 1) & 1u, kWait));
+          if (!__all_sync(0xffffffffu, ok)) {
+            aborted = true;
+            break;
+          }
+          const uint8_t* src = sRaw + (st * 2 + v) * kRawBytes + ch * 16;
+          uint8_t* dst = (v ? sV : sK) + st * kTileBytes + (ch >> 2) * kBoxBytes;
+          const int live = v ? kv_end - (t_lo + j) * kTile : kTile;   // V rows behind the last key: zeros
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int row = u * 16 + row_of;
+            uint4 w = *reinterpret_cast<const uint4*>(src + row * 128);
+            if (row >= live || s_bad[st * 2 + (u >> 2)]) w = make_uint4(0, 0, 0, 0);
+            uint4 h[2];
+            halves_of(w.x, h[0].x, h[0].y);
+            halves_of(w.y, h[0].z, h[0].w);
+            halves_of(w.z, h[1].x, h[1].y);
+            halves_of(w.w, h[1].z, h[1].w);
+            // the 32 bytes are chunks 2 ch and 2 ch + 1 of the box; the upper box's lanes store the odd one first,
+            // so that eight lanes never meet in a bank
+            const int q = (2 * ch) & 7, odd = ch >> 2;
+            *reinterpret_cast<uint4*>(dst + row * 128 + (((q + odd) ^ (row & 7)) << 4)) = odd ? h[1] : h[0];
+            *reinterpret_cast<uint4*>(dst + row * 128 + (((q + 1 - odd) ^ (row & 7)) << 4)) = odd ? h[0] : h[1];
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if ((tid & 31) == 0) {
+            mbar_arrive(v ? &v_full[st] : &k_full[st]);
+            if (v) mbar_arrive(&raw_empty[st]);
+          }
+        }
+      }
+      if (aborted) {
+        *s_abort = 1;
+        set_err(a.err, NLD_DEVERR_TIMEOUT);
+      }
+    }
+  }
+
+  // ------------------------------------------------------- the streams' partials --
+  __syncthreads();   // every product is done; loads too, unless a wait ran out
+  if (load_thr && *s_abort) {   // the copies still in flight land before the rings are overlaid
+    for (int t = max(0, n_issued - 3); t < n_issued; ++t) {
+      if constexpr (kQ8) {
+        mbar_wait(&raw_full[t % 2], static_cast<uint32_t>(t / 2) & 1u, kWait);
+      } else {
+        mbar_wait(&k_full[t % 3], static_cast<uint32_t>(t / 3) & 1u, kWait);
+        mbar_wait(&v_full[t % 3], static_cast<uint32_t>(t / 3) & 1u, kWait);
+      }
+    }
+  }
+  __syncthreads();
+  float* sO = reinterpret_cast<float*>(smem);   // [128][128]; float4 s of row r at s ^ (r % 32)
+  float* sML = sO + 128 * 128;                  // [128][2] max, sum
+  const bool have = softmax_thr && ntile > x && !*s_abort;
+  const uint32_t o_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 + x * 128;
+  // stream 0 leaves its row, stream 1 adds its own
+  auto leave = [&](bool add) {
+    float w0 = 0.f, w1 = have ? 1.f : 0.f, M = have ? m_ref : -INFINITY, L = have ? l_sum : 0.f;
+    if (add) {
+      const float2 ml = *reinterpret_cast<const float2*>(sML + 2 * r);
+      const float top = fmaxf(M, ml.x);
+      w0 = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+      w1 = M == -INFINITY ? 0.f : exp2f(M - top);
+      M = top;
+      L = w0 * ml.y + w1 * L;
+    }
+    const bool take = __any_sync(0xffffffffu, w1 != 0.f);   // (a stream without a tile has no O)
+#pragma unroll 2
+    for (int u = 0; u < 8; ++u) {
+      float o[16];
+      if (take) {
+        tmem_ld16(o_at + u * 16, o);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 16; k += 4) {
+        float4* at = reinterpret_cast<float4*>(sO + r * 128 + ((((u * 16 + k) >> 2) ^ (r & 31)) << 2));
+        float4 v = w1 != 0.f ? make_float4(o[k] * w1, o[k + 1] * w1, o[k + 2] * w1, o[k + 3] * w1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (add && w0 != 0.f) {
+          const float4 z = *at;
+          v = make_float4(fmaf(z.x, w0, v.x), fmaf(z.y, w0, v.y), fmaf(z.z, w0, v.z), fmaf(z.w, w0, v.w));
+        }
+        *at = v;
+      }
+    }
+    *reinterpret_cast<float2*>(sML + 2 * r) = make_float2(M, L);
+  };
+  if (softmax_thr && x == 0) leave(false);
+  __syncthreads();
+  if (softmax_thr && x == 1) leave(true);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftmax / 32) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+
+  // the splits' partials: rank q of the cluster finishes rows q, q + S, .., a warp each
+  const int S = a.S;
+  if (S > 1) cluster_sync();
+  float vscale = 1.f;
+  if constexpr (kQ8) vscale = a.v_scale[g];
+  if constexpr (kShare == kOwnPass) pdl_wait();   // the prefix pass has written its partials
+  const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int d4 = tid & 31;
+  const uint32_t o_base = smem_u32(sO), ml_base = smem_u32(sML);
+  for (int rr = rank + warp * S; rr < rows; rr += S * (W::kThreads / 32)) {
+    const uint32_t o_off = (rr * 128 + ((d4 ^ (rr & 31)) << 2)) * 4;
+    float M, L;
+    float4 acc;
+    if (S == 1) {
+      M = sML[2 * rr];
+      L = sML[2 * rr + 1];
+      acc = *reinterpret_cast<const float4*>(reinterpret_cast<const uint8_t*>(sO) + o_off);
+    } else {
+      float2 ml[8];
+      float4 ov[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        ml[q] = make_float2(-INFINITY, 0.f);
+        ov[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q < S) {
+          ml[q] = ld_dsmem_f2(dsmem_addr(ml_base, q) + rr * 8);
+          ov[q] = ld_dsmem_f4(dsmem_addr(o_base, q) + o_off);
+        }
+      }
+      M = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) M = fmaxf(M, ml[q].x);
+      L = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (ml[q].x != -INFINITY) {
+          const float w = exp2f(ml[q].x - M);
+          L += w * ml[q].y;
+          acc.x += w * ov[q].x;
+          acc.y += w * ov[q].y;
+          acc.z += w * ov[q].z;
+          acc.w += w * ov[q].w;
+        }
+    }
+    const int row = r0 + rr, pos = row / a.G;
+    const size_t at = (static_cast<size_t>(b) * a.m + pos) * a.Hq + static_cast<size_t>(g) * a.G + (row - pos * a.G);
+    if constexpr (kShare != 0)
+      if (share_merge<kShare>(a.part_o, a.part_ml, at, d4, M, L, acc)) continue;
+    const float k = L > 0.f ? vscale / L : 0.f;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * 128 + 4 * d4) =
+        make_uint2(pack16<false>(acc.x * k, acc.y * k), pack16<false>(acc.z * k, acc.w * k));
+  }
+  if (S > 1) cluster_sync();   // peers may still be reading this CTA's shared memory
+}
+
+using WideKernel = void (*)(const CUtensorMap, const AttnWideArgs);
+WideKernel wide_kernel(int share) {
+  if (share == kPrefixPass) return attn_wide_kernel<__nv_bfloat16, kPrefixPass>;
+  if (share == kOwnPass) return attn_wide_kernel<__nv_bfloat16, kOwnPass>;
+  return attn_wide_kernel<__nv_fp8_storage_t, 0>;
+}
+int bytes_of(int share) { return share ? wide_bytes<__nv_bfloat16>() : wide_bytes<__nv_fp8_storage_t>(); }
+int threads_of(int share) { return share ? Wide<__nv_bfloat16>::kThreads : Wide<__nv_fp8_storage_t>::kThreads; }
+static_assert(kQBytes + 4 * kTileBytes >= (128 * 128 + 256) * 4, "the partials overlay Q and the rings");
+
+// Clusters of S CTAs that can be resident at once (asked once per device and S).
+cudaError_t wide_capacity(int share, int S, int sms, int* n) {
+  static int cache[16][3][9];
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  int* c = dev < 16 ? &cache[dev][share][S] : nullptr;
+  if (c && *c) {
+    *n = *c;
+    return cudaSuccess;
+  }
+  if ((e = cudaFuncSetAttribute(wide_kernel(share), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes_of(share))) != cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(S * (sms / S));
+  cfg.blockDim = dim3(threads_of(share));
+  cfg.dynamicSmemBytes = bytes_of(share);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaOccupancyMaxActiveClusters(n, wide_kernel(share), &cfg)) != cudaSuccess) return e;
+  *n = std::max(1, *n);
+  if (c) *c = *n;
+  return cudaSuccess;
+}
+
+}  // namespace
+
+// Query tiles and KV splits of a launch.
+cudaError_t attn_wide_plan(int batch, int max_len, int sms, AttnWideArgs& a) {
+  const int all = a.m * a.G;
+  a.q_tiles = (all + 127) / 128;
+  a.rows = (all + a.q_tiles - 1) / a.q_tiles;
+  const long long units = static_cast<long long>(batch) * a.q_tiles * a.Hkv;
+  const int tiles = (max_len + kTile - 1) / kTile;
+  // The fewest rounds of resident clusters times a round's length, a tile 1 and the rest of a CTA 8
+  double best = 0;
+  for (int S = 1; S <= 8 && S <= tiles; ++S) {
+    int cap = 1;
+    const cudaError_t e = wide_capacity(a.share, S, sms, &cap);
+    if (e != cudaSuccess) return e;
+    const double cost = static_cast<double>((units + cap - 1) / cap) * ((tiles + S - 1) / S + 8.0);
+    if (S == 1 || cost < best) {
+      best = cost;
+      a.S = S;
+    }
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_attention_wide(cudaStream_t st, const CUtensorMap* tmKV, const AttnWideArgs& a, int batch, bool pdl) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.S, a.Hkv, batch * a.q_tiles);
+  cfg.blockDim = dim3(threads_of(a.share));
+  cfg.dynamicSmemBytes = bytes_of(a.share);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, wide_kernel(a.share), *tmKV, a);
+}
+
+}  // namespace nld

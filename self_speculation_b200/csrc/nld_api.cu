@@ -2250,6 +2250,9 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
   return NLD_OK;
 }
 
+// Rows of a kv head (positions x heads) up to which the kernel for small query tiles serves a call.
+constexpr int kSmallRowsQ8 = 32, kSmallRowsShared = 64;
+
 // Argument checks common to the attention operators below.
 static nld_status attn_check(const void* d_q, const void* d_kv_pool, const int32_t* d_page_table, int pages_per_seq,
                              int n_pages, const int32_t* d_lens, int batch, int m, int n_q_heads, int n_kv_heads,
@@ -2278,26 +2281,40 @@ nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float*
   TRY(attn_check(d_q, d_kv_pool, d_page_table, pages_per_seq, n_pages, d_lens, batch, m, n_q_heads, n_kv_heads,
                  head_dim, block_size, max_len, d_out));
   if (!d_k_scale || !d_v_scale) return fail(nullptr, NLD_ERR_ARG, "NULL scale pointer");
-  AttnSmallArgs a{};
-  a.m = m;
-  a.Hq = n_q_heads;
-  a.Hkv = n_kv_heads;
-  a.G = n_q_heads / n_kv_heads;
-  attn_small_plan(batch, max_len, device_sms(), a);
-  if (static_cast<long long>(batch) * a.r_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
-  a.q = d_q;
-  a.out = d_out;
-  a.pool = d_kv_pool;
-  a.k_scale = d_k_scale;
-  a.v_scale = d_v_scale;
-  a.lens = d_lens;
-  a.page_table = d_page_table;
-  a.pps = pages_per_seq;
-  a.n_pages = n_pages;
-  a.block_size = block_size;
-  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
-  a.err = d_err;
-  const cudaError_t e = launch_attention_small(static_cast<cudaStream_t>(cuda_stream), a, batch, false);
+  const int G = n_q_heads / n_kv_heads, sms = device_sms();
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  auto fill = [&](auto& a) {
+    a.q = d_q;
+    a.out = d_out;
+    a.pool = d_kv_pool;
+    a.k_scale = d_k_scale;
+    a.v_scale = d_v_scale;
+    a.lens = d_lens;
+    a.page_table = d_page_table;
+    a.pps = pages_per_seq;
+    a.n_pages = n_pages;
+    a.m = m;
+    a.Hq = n_q_heads;
+    a.Hkv = n_kv_heads;
+    a.G = G;
+    a.block_size = block_size;
+    a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
+    a.err = d_err;
+  };
+  cudaError_t e;
+  if (static_cast<long long>(m) * G <= kSmallRowsQ8) {
+    AttnSmallArgs a{};
+    fill(a);
+    attn_small_plan(batch, max_len, sms, a);
+    if (static_cast<long long>(batch) * a.r_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
+    e = launch_attention_small(st, a, batch, false);
+  } else {
+    AttnWideArgs a{};
+    fill(a);
+    if ((static_cast<long long>(m) * G + 127) / 128 * batch > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
+    const CUtensorMap none{};
+    if ((e = attn_wide_plan(batch, max_len, sms, a)) == cudaSuccess) e = launch_attention_wide(st, &none, a, batch, false);
+  }
   if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
   return NLD_OK;
 }
@@ -2332,12 +2349,11 @@ nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const in
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   CUtensorMap map;
   bool have_map = false;
-  // One pass: rows of `seqs` sequences of `rows` positions each, over max_len keys at most.  Up to
-  // kSmallRows rows of a kv head take the kernel for small query tiles, more the planner's choice.
-  constexpr int kSmallRows = 64;
+  // One pass: rows of `seqs` sequences of `rows` positions each, over max_keys keys at most.  A kernel forced by the
+  // profiling hook serves both passes.
   auto pass = [&](int share, int seqs, int rows, const int32_t* table, int pps, int max_keys, bool pdl, bool launch) -> nld_status {
     cudaError_t e = cudaSuccess;
-    if (g_attn_kernel.load() == 0 && static_cast<long long>(rows) * G <= kSmallRows) {
+    if (g_attn_kernel.load() == 0 && static_cast<long long>(rows) * G <= kSmallRowsShared) {
       AttnSmallArgs a{};
       a.q = d_q;
       a.out = d_out;
@@ -2361,38 +2377,61 @@ nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const in
       if (static_cast<long long>(seqs) * a.r_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
       if (launch) e = launch_attention_small(st, a, seqs, pdl);
     } else {
-      if (!have_map) {
+      if (!have_map && !make_map_bf16(&map, d_kv_pool, 128, static_cast<uint64_t>(n_pages) * 2 * n_kv_heads * kPage, kPage))
+        return fail(nullptr, NLD_ERR_CUDA, "tensor map encode failed (pool)");
+      have_map = true;
+      if (g_attn_kernel.load() == 0) {
+        AttnWideArgs a{};
+        a.q = d_q;
+        a.out = d_out;
+        a.lens = d_lens;
+        a.page_table = table;
+        a.pps = pps;
+        a.n_pages = n_pages;
+        a.m = rows;
+        a.Hq = n_q_heads;
+        a.Hkv = n_kv_heads;
+        a.G = G;
+        a.block_size = block_size;
+        a.scale_log2 = scale_log2;
+        a.share = share;
+        a.key_end = shared_len;
+        a.part_o = part_o;
+        a.part_ml = part_ml;
+        a.err = d_err;
+        if ((static_cast<long long>(rows) * G + 127) / 128 * seqs > 65535)
+          return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
+        e = attn_wide_plan(seqs, max_keys, sms, a);
+        if (e == cudaSuccess && launch) e = launch_attention_wide(st, &map, a, seqs, pdl);
+      } else {
         if ((e = init_shared_attention_attributes()) != cudaSuccess) {
           cudaGetLastError();
           return fail(nullptr, NLD_ERR_CUDA, "setting kernel shared-memory limits failed: %s", cudaGetErrorString(e));
         }
-        if (!make_map_bf16(&map, d_kv_pool, 128, static_cast<uint64_t>(n_pages) * 2 * n_kv_heads * kPage, kPage))
-          return fail(nullptr, NLD_ERR_CUDA, "tensor map encode failed (pool)");
-        have_map = true;
+        AttnArgs a{};
+        a.q = d_q;
+        a.out = d_out;
+        a.out_ld = static_cast<size_t>(n_q_heads) * 128;
+        a.m = rows;
+        a.Hq = n_q_heads;
+        a.Hkv = n_kv_heads;
+        a.hd = 128;
+        a.lens = d_lens;
+        a.page_table = table;
+        a.pps = pps;
+        a.block_size = block_size;
+        a.scale_log2 = scale_log2;
+        a.share = share;
+        a.key_end = shared_len;
+        a.part_o = part_o;
+        a.part_ml = part_ml;
+        a.err = d_err;
+        attn_plan(seqs, rows, n_q_heads, n_kv_heads, max_keys, sms, a,
+                  [](int S, int NW, int stages, int tc) { return attn_device_capacity(false, S, NW, stages, tc); }, 0, 0,
+                  g_attn_kernel.load(), g_attn_tile.load(), false);
+        if (static_cast<long long>(seqs) * a.q_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
+        if (launch) e = launch_attention_mma(st, &map, a, seqs, pdl);
       }
-      AttnArgs a{};
-      a.q = d_q;
-      a.out = d_out;
-      a.out_ld = static_cast<size_t>(n_q_heads) * 128;
-      a.m = rows;
-      a.Hq = n_q_heads;
-      a.Hkv = n_kv_heads;
-      a.hd = 128;
-      a.lens = d_lens;
-      a.page_table = table;
-      a.pps = pps;
-      a.block_size = block_size;
-      a.scale_log2 = scale_log2;
-      a.share = share;
-      a.key_end = shared_len;
-      a.part_o = part_o;
-      a.part_ml = part_ml;
-      a.err = d_err;
-      attn_plan(seqs, rows, n_q_heads, n_kv_heads, max_keys, sms, a,
-                [](int S, int NW, int stages, int tc) { return attn_device_capacity(false, S, NW, stages, tc); }, 0, 0,
-                g_attn_kernel.load(), g_attn_tile.load(), false);
-      if (static_cast<long long>(seqs) * a.q_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
-      if (launch) e = launch_attention_mma(st, &map, a, seqs, pdl);
     }
     if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
     return NLD_OK;

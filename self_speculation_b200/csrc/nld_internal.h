@@ -215,6 +215,24 @@ struct AttnSmallArgs {
   int* err;
 };
 
+// The same for wide query tiles, on tcgen05.
+struct AttnWideArgs {
+  const void* q;                // [batch, m, Hq, 128] bf16
+  void* out;
+  const void* pool;             // e4m3 (bf16: the tensor map)
+  const float *k_scale, *v_scale;
+  const int* lens;
+  const int* page_table;
+  int pps, n_pages;
+  int m, Hq, Hkv, G, block_size;
+  int q_tiles, rows, S;         // query tiles of a sequence, rows of one, KV splits (cluster size)
+  float scale_log2;
+  int share, key_end;
+  float* part_o;
+  float2* part_ml;
+  int* err;
+};
+
 // Token sampling (nld_sample).
 struct SampleArgs {
   const void* logits;           // rows ld elements apart
@@ -247,6 +265,8 @@ cudaError_t init_shared_attention_attributes();
 cudaError_t launch_qkv_write(cudaStream_t st, const QkvWriteArgs& a, int dtype, int kv_dtype);
 void attn_small_plan(int batch, int max_len, int sms, AttnSmallArgs& a);
 cudaError_t launch_attention_small(cudaStream_t st, const AttnSmallArgs& a, int batch, bool pdl);
+cudaError_t attn_wide_plan(int batch, int max_len, int sms, AttnWideArgs& a);
+cudaError_t launch_attention_wide(cudaStream_t st, const CUtensorMap* tmKV, const AttnWideArgs& a, int batch, bool pdl);
 cudaError_t launch_sample(cudaStream_t st, const SampleArgs& a, int dtype, int sms);
 
 struct EmbedArgs {
