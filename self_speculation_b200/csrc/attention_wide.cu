@@ -4,16 +4,18 @@
 //
 //   o = softmax(q K^T / sqrt(hd) + mask) V;   e4m3: K = k_scale[g] k8,  V = v_scale[g] v8
 //
-// One CTA per (KV split, kv head, sequence x query tile); row = position * G + head.  A tile of 128 keys
-// costs 1024 cycles of tensor core (S = Q K^T and O += P V, 128 x 128 x 128 each) and as many of the exponential
-// unit (16 a cycle and SM), so the two have to run side by side: the even and the odd key tiles are two
+// One CTA per (KV split, kv head, sequence x query tile); row = position * G + head.  128 keys cost 1024
+// cycles of tensor core (S = Q K^T and O += P V, 128 x 128 x 128 each) and as many of the exponential
+// unit (16 a cycle and SM), so the two have to run side by side: the even and the odd pages are two
 // streams, each with its own S, O, running max and sum, its own four softmax warps (a thread per row) and its
-// own issuing thread.  While one stream's softmax runs, the other's products do.  Tensor memory is full: S of
-// both streams (P is written over S, in 16 bits), O of both.  The streams' partials meet in shared memory at
-// the end, those of the KV splits over the cluster's distributed shared memory, in a fixed order.
+// own issuing thread.  A stream has two S buffers: the scores of its next page are there when the softmax is
+// done with one, and O += P V runs behind (P is written over its S, in 16 bits).  That fills tensor memory: 4 x 64
+// columns of S, 2 x 128 of O.  With one S of 128 keys a stream, a stream waited 2400 of 6000 cycles a
+// tile for P V and then S.  The streams' partials meet in shared memory at the end, those of the KV splits
+// over the cluster's distributed shared memory, in a fixed order.
 //
-// bf16: K and V come by TMA into rings of three tiles.  e4m3: a page's K (or V) rows of a kv head are 8 KB in a
-// row and come by bulk copies; four warps turn them into fp16 tiles (exact), two of K and two of V, in the
+// bf16: K and V come by TMA into rings of six pages.  e4m3: a page's K (or V) rows of a kv head are 8 KB in a
+// row and come by bulk copies; four warps turn them into fp16 tiles (exact), four of K and four of V, in the
 // swizzled layout of the descriptors.  K's place frees when S is done, V's when O is.  Q's rows are scaled by a power
 // of two into fp16's range there, and P is rounded to fp16 (attention_small.cu has the errors); over the bf16
 // cache P is rounded to bf16.  The maximum that exponents refer to moves only when it has grown by 2^8, so O is
@@ -32,25 +34,25 @@ namespace nld {
 
 namespace {
 
-constexpr int kTile = 128;                   // keys of a tile
-constexpr int kTileBytes = kTile * 256;      // K (or V) of a tile in 16 bits: [2 boxes of 64 dims][128 keys][128 B]
+constexpr int kTile = kPage;                 // keys of a tile
+constexpr int kTileBytes = kTile * 256;      // K (or V) of a tile in 16 bits: [2 boxes of 64 dims][64 keys][128 B]
 constexpr int kBoxBytes = kTileBytes / 2;
-constexpr int kRawBytes = kTile * 128;       // the same in e4m3: [128 keys][128 B]
+constexpr int kRawBytes = kTile * 128;       // the same in e4m3: [64 keys][128 B]
 constexpr int kQBytes = 128 * 256;           // [2 boxes][128 rows][128 B]
-constexpr int kSoftmax = 256;                // threads: two streams of 128
+constexpr int kSoftmax = 256;                // threads: two streams of 128, a row each
 constexpr float kMove = 8.f;                 // log2 units
 constexpr uint64_t kWait = 2000000000ull;
 
 template <typename E>
 struct Wide {   // bf16
   static constexpr bool kQ8 = false;
-  static constexpr int kK = 3, kV = 3, kRaw = 0;        // tiles of K, of V, raw ones
+  static constexpr int kK = 6, kV = 6, kRaw = 0;        // tiles of K, of V, raw ones
   static constexpr int kThreads = kSoftmax + 96;        // two issuing warps, a loading one
 };
 template <>
 struct Wide<__nv_fp8_storage_t> {
   static constexpr bool kQ8 = true;
-  static constexpr int kK = 2, kV = 2, kRaw = 2;
+  static constexpr int kK = 4, kV = 4, kRaw = 4;
   static constexpr int kThreads = kSoftmax + 96 + 128;   // and four converting ones
 };
 template <typename E>
@@ -103,6 +105,24 @@ NLD_DEV float exp2_hw(float x) {   // relative error about 2^-22; 2^-inf = 0
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two fp32 numbers worked on by one instruction.
+typedef unsigned long long f2;
+NLD_DEV f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+NLD_DEV void unpair(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+NLD_DEV f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+NLD_DEV f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 template <bool kHalf>
 NLD_DEV uint32_t pack16(float lo, float hi) {
   if constexpr (kHalf) {
@@ -138,18 +158,18 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   uint8_t* sRaw = sV + W::kV * kTileBytes;     // [kRaw][K, V]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sRaw + W::kRaw * 2 * kRawBytes);
   uint64_t* k_full = bars;             // [kK] tile of K there
-  uint64_t* k_empty = bars + 3;        // [kK] S of the tile done
-  uint64_t* v_full = bars + 6;         // [kV]
-  uint64_t* v_empty = bars + 9;        // [kV] O += P V of the tile done
-  uint64_t* raw_full = bars + 12;      // [kRaw] bytes landed
-  uint64_t* raw_empty = bars + 14;     // [kRaw] converted
-  uint64_t* s_full = bars + 16;        // [2] by stream: S written
-  uint64_t* p_full = bars + 18;        // [2] P written, S read
-  uint64_t* pv_done = bars + 20;       // [2] O += P V done
-  uint64_t* fin = bars + 22;           // every product done
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 23);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(bars + 24);
-  int* s_bad = reinterpret_cast<int*>(bars + 25);   // [kRaw][2] the page is outside the pool
+  uint64_t* k_empty = bars + 6;        // [kK] S of the tile done
+  uint64_t* v_full = bars + 12;        // [kV]
+  uint64_t* v_empty = bars + 18;       // [kV] O += P V of the tile done
+  uint64_t* raw_full = bars + 24;      // [kRaw] bytes landed
+  uint64_t* raw_empty = bars + 28;     // [kRaw] converted
+  uint64_t* s_full = bars + 32;        // [stream][buffer] S written
+  uint64_t* p_full = bars + 36;        // [stream][buffer] P written
+  uint64_t* pv_done = bars + 40;       // [stream][buffer] O += P V done
+  uint64_t* fin = bars + 44;           // every product done
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 45);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(bars + 46);
+  int* s_bad = reinterpret_cast<int*>(bars + 47);   // [kRaw] the page is outside the pool
 
   const int tid = threadIdx.x, warp = tid >> 5;
   const int split = blockIdx.x, g = blockIdx.y;
@@ -173,7 +193,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
@@ -203,10 +223,9 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   };
   const int kv_end = seen_by(r0 + rows - 1);   // the last row sees the most
   const int n_pages = (kv_end + kPage - 1) / kPage;
-  const int n_tiles = (kv_end + kTile - 1) / kTile;
-  const int per = (n_tiles + a.S - 1) / a.S;
+  const int per = (n_pages + a.S - 1) / a.S;
   const int t_lo = split * per;
-  const int ntile = max(0, min(n_tiles, t_lo + per) - t_lo);
+  const int ntile = max(0, min(n_pages, t_lo + per) - t_lo);
 
   // Q into shared memory, K-major in 128-byte-swizzled boxes: thread (stream x, row r) writes box x of row r
   const int x = tid >> 7, r = tid & 127;   // softmax threads
@@ -262,60 +281,44 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   if (load_thr) {
     // ---------------------------------------------------------------- loads --
     for (int j = 0; j < ntile; ++j) {
-      int page[2];
-      bool bad[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int p = 2 * (t_lo + j) + h;   // a page past the keys: the first page again, its keys masked
-        page[h] = table[p < n_pages ? p : p - 1];
-        bad[h] = page[h] < 0 || page[h] >= a.n_pages;
-        if (bad[h]) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
-      }
+      const int page = table[t_lo + j];
+      const bool bad = page < 0 || page >= a.n_pages;
+      if (bad) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
       if constexpr (kQ8) {
-        const int st = j % 2;
-        if (j >= 2 && (*s_abort || !mbar_wait(&raw_empty[st], static_cast<uint32_t>(j / 2 - 1) & 1u, kWait))) {
+        const int st = j % W::kRaw;
+        if (j >= W::kRaw && (*s_abort || !mbar_wait(&raw_empty[st], static_cast<uint32_t>(j / W::kRaw - 1) & 1u, kWait))) {
           aborted = true;
           break;
         }
         ++n_issued;
-        s_bad[st * 2] = bad[0];
-        s_bad[st * 2 + 1] = bad[1];
+        s_bad[st] = bad;
         mbar_arrive_expect_tx(&raw_full[st], 2 * kRawBytes);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint8_t* kp = static_cast<const uint8_t*>(a.pool) +
-                              (static_cast<size_t>(bad[h] ? 0 : page[h]) * 2 * a.Hkv + g) * (kPage * 128);
-          bulk_load(sRaw + (st * 2) * kRawBytes + h * (kRawBytes / 2), kp, kRawBytes / 2, &raw_full[st]);
-          bulk_load(sRaw + (st * 2 + 1) * kRawBytes + h * (kRawBytes / 2), kp + static_cast<size_t>(a.Hkv) * (kPage * 128),
-                    kRawBytes / 2, &raw_full[st]);
-        }
+        const uint8_t* kp = static_cast<const uint8_t*>(a.pool) + (static_cast<size_t>(bad ? 0 : page) * 2 * a.Hkv + g) * kRawBytes;
+        bulk_load(sRaw + (st * 2) * kRawBytes, kp, kRawBytes, &raw_full[st]);
+        bulk_load(sRaw + (st * 2 + 1) * kRawBytes, kp + static_cast<size_t>(a.Hkv) * kRawBytes, kRawBytes, &raw_full[st]);
       } else {
-        const int st = j % 3;
-        if (j >= 3 && (*s_abort || !mbar_wait(&k_empty[st], static_cast<uint32_t>(j / 3 - 1) & 1u, kWait))) {
+        const int st = j % W::kK;
+        if (j >= W::kK && (*s_abort || !mbar_wait(&k_empty[st], static_cast<uint32_t>(j / W::kK - 1) & 1u, kWait))) {
           aborted = true;
           break;
         }
         // (a page outside the pool: rows outside the tensor, which read as zeros)
         mbar_arrive_expect_tx(&k_full[st], kTileBytes);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int box = 0; box < 2; ++box)
-            tma_load_2d(sK + st * kTileBytes + box * kBoxBytes + h * (kPage * 128), &tmKV, &k_full[st], box * 64,
-                        bad[h] ? -kPage : (page[h] * 2 * a.Hkv + g) * kPage);
-        if (j >= 3 && (*s_abort || !mbar_wait(&v_empty[st], static_cast<uint32_t>(j / 3 - 1) & 1u, kWait))) {
-          mbar_wait(&k_full[st], static_cast<uint32_t>(j / 3) & 1u, kWait);   // the copies in flight land
+        for (int box = 0; box < 2; ++box)
+          tma_load_2d(sK + st * kTileBytes + box * kBoxBytes, &tmKV, &k_full[st], box * 64,
+                      bad ? -kPage : (page * 2 * a.Hkv + g) * kPage);
+        if (j >= W::kV && (*s_abort || !mbar_wait(&v_empty[st], static_cast<uint32_t>(j / W::kV - 1) & 1u, kWait))) {
+          mbar_wait(&k_full[st], static_cast<uint32_t>(j / W::kK) & 1u, kWait);   // the copies in flight land
           aborted = true;
           break;
         }
         ++n_issued;
         mbar_arrive_expect_tx(&v_full[st], kTileBytes);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int box = 0; box < 2; ++box)
-            tma_load_2d(sV + st * kTileBytes + box * kBoxBytes + h * (kPage * 128), &tmKV, &v_full[st], box * 64,
-                        bad[h] ? -kPage : ((page[h] * 2 + 1) * a.Hkv + g) * kPage);
+        for (int box = 0; box < 2; ++box)
+          tma_load_2d(sV + st * kTileBytes + box * kBoxBytes, &tmKV, &v_full[st], box * 64,
+                      bad ? -kPage : ((page * 2 + 1) * a.Hkv + g) * kPage);
       }
     }
     if (aborted) {
@@ -325,28 +328,32 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   } else if (issue_thr) {
     // ------------------------------------------- products of stream y: tiles y, y + 2, .. --
     const int y = tid == kSoftmax ? 0 : 1;
-    constexpr uint32_t kF16 = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);   // fp32 accumulator, 128 x 128, fp16
-    constexpr uint32_t idS = kQ8 ? kF16 : idesc_bf16_f32(128, 128);
-    constexpr uint32_t idO = idS | (1u << 16);   // B (V) MN-major
-    const uint32_t s_col = tmem + y * 128, o_col = tmem + 256 + y * 128;
-    for (int j = y, i = 0; j < ntile; j += 2, ++i) {
-      const int ks = j % W::kK, vs = j % W::kV;
-      // S over the P of the stream's tile before, once O += P V has read it
+    constexpr uint32_t kKind = kQ8 ? (1u << 4) : (1u << 4) | (1u << 7) | (1u << 10);   // fp32 accumulator; fp16 or bf16
+    constexpr uint32_t idS = kKind | ((static_cast<uint32_t>(kTile) >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t idO = kKind | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);   // B (V) MN-major
+    const uint32_t o_col = tmem + 256 + y * 128;
+    const int mine = ntile > y ? (ntile - y + 1) / 2 : 0;   // tiles of the stream
+    // S of the stream's tile i into buffer i & 1, free once O += P V of tile i - 2 has read P there
+    auto s_step = [&](int i) -> bool {
+      const int j = y + 2 * i, ks = j % W::kK, u = y * 2 + (i & 1);
       if (*s_abort || !mbar_wait(&k_full[ks], static_cast<uint32_t>(j / W::kK) & 1u, kWait) ||
-          (i > 0 && !mbar_wait(&pv_done[y], static_cast<uint32_t>(i - 1) & 1u, kWait))) {
-        aborted = true;
-        break;
-      }
+          (i >= 2 && !mbar_wait(&pv_done[u], static_cast<uint32_t>((i - 2) >> 1) & 1u, kWait)))
+        return false;
       tc_fence_after();
 #pragma unroll
       for (int box = 0; box < 2; ++box)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          tc_mma_f16(s_col, sdesc_k_sw128(smem_u32(sQ + box * (kQBytes / 2))) + 2 * kk,
+          tc_mma_f16(tmem + u * kTile, sdesc_k_sw128(smem_u32(sQ + box * (kQBytes / 2))) + 2 * kk,
                      sdesc_k_sw128(smem_u32(sK + ks * kTileBytes + box * kBoxBytes)) + 2 * kk, idS, (box > 0 || kk > 0) ? 1u : 0u);
       tc_commit(&k_empty[ks]);
-      tc_commit(&s_full[y]);
-      if (!mbar_wait(&p_full[y], static_cast<uint32_t>(i) & 1u, kWait) || *s_abort ||
+      tc_commit(&s_full[u]);
+      return true;
+    };
+    for (int i = 0; i < min(2, mine) && !aborted; ++i) aborted = !s_step(i);
+    for (int i = 0; i < mine && !aborted; ++i) {
+      const int j = y + 2 * i, vs = j % W::kV, u = y * 2 + (i & 1);
+      if (*s_abort || !mbar_wait(&p_full[u], static_cast<uint32_t>(i >> 1) & 1u, kWait) ||
           !mbar_wait(&v_full[vs], static_cast<uint32_t>(j / W::kV) & 1u, kWait)) {
         aborted = true;
         break;
@@ -354,10 +361,11 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)   // 16 keys: 8 columns of P
-        tc_mma_ts(o_col, s_col + k * 8, desc_mn(smem_u32(sV + vs * kTileBytes + k * 2048), kBoxBytes, 1024), idO,
+        tc_mma_ts(o_col, tmem + u * kTile + k * 8, desc_mn(smem_u32(sV + vs * kTileBytes + k * 2048), kBoxBytes, 1024), idO,
                   (i > 0 || k > 0) ? 1u : 0u);
       tc_commit(&v_empty[vs]);
-      tc_commit(&pv_done[y]);
+      tc_commit(&pv_done[u]);
+      if (i + 2 < mine) aborted = !s_step(i + 2);
     }
     if (aborted) {
       *s_abort = 1;
@@ -370,80 +378,74 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     // ----------------------------------------------------------- softmax of stream x, row r --
     const int seen = r < rows ? seen_by(r0 + r) : 0;
     const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lane + x * 128, o_at = tmem + lane + 256 + x * 128;
-    for (int j = x, i = 0; j < ntile; j += 2, ++i) {
+    const uint32_t o_at = tmem + lane + 256 + x * 128;
+    const f2 c2 = pair(c, c);
+    const int mine = ntile > x ? (ntile - x + 1) / 2 : 0;   // tiles of the stream
+    for (int i = 0; i < mine; ++i) {
+      const int j = x + 2 * i, u = x * 2 + (i & 1);
+      const uint32_t s_at = tmem + lane + u * kTile;
       // tcgen05.ld / st are for whole warps: every exit of this loop is taken by the warp together
-      if (!__all_sync(0xffffffffu, !*s_abort && mbar_wait(&s_full[x], static_cast<uint32_t>(i) & 1u, kWait))) {
+      if (!__all_sync(0xffffffffu, !*s_abort && mbar_wait(&s_full[u], static_cast<uint32_t>(i >> 1) & 1u, kWait))) {
         aborted = true;
         break;
       }
       tc_fence_after();
-      const int left = seen - (t_lo + j) * kTile;   // keys of the tile that the row sees
-      const bool whole = __all_sync(0xffffffffu, left >= kTile);
       uint32_t s[2][32];
-      float mx = -INFINITY;
       tmem_ld32_nowait(s_at, s[0]);
+      tmem_ld32_nowait(s_at + 32, s[1]);
+      tmem_wait_ld(s[0]);
+      tmem_wait_ld(s[1]);
+      const int left = seen - (t_lo + j) * kTile;   // keys of the tile that the row sees
+      if (!__all_sync(0xffffffffu, left >= kTile)) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        tmem_wait_ld(s[u & 1]);
-        if (u < 3) tmem_ld32_nowait(s_at + (u + 1) * 32, s[(u + 1) & 1]);
-        float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (whole) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(s[u & 1][k]));
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], u * 32 + k < left ? __uint_as_float(s[u & 1][k]) : -INFINITY);
-        }
-        mx = fmaxf(mx, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
+        for (int k = 0; k < kTile; ++k)
+          if (k >= left) s[k >> 5][k & 31] = 0xff800000u;
       }
-      tmem_ld32_nowait(s_at, s[0]);   // once more for the exponents
-      mx *= c;
+      float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < kTile; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(s[k >> 5][k & 31]));
+      const float mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;
       const bool move = mx > m_ref + kMove;
       const bool scale_o = move && m_ref != -INFINITY;
       if (__any_sync(0xffffffffu, scale_o)) {   // (i > 0: m_ref was set)
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(i - 1) & 1u, kWait))) {
-          tmem_wait_ld(s[0]);
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[u ^ 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, kWait))) {
           aborted = true;
           break;
         }
         tc_fence_after();
-        tmem_wait_ld(s[0]);
         const float alpha = scale_o ? exp2f(m_ref - mx) : 1.f;
 #pragma unroll 1
-        for (int u = 0; u < 8; ++u) {
+        for (int q = 0; q < 8; ++q) {
           float o[16];
           uint32_t w[16];
-          tmem_ld16(o_at + u * 16, o);
+          tmem_ld16(o_at + q * 16, o);
 #pragma unroll
           for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * alpha);
-          tmem_st16u(o_at + u * 16, w);
+          tmem_st16u(o_at + q * 16, w);
         }
         tmem_wait_st();
         l_sum *= alpha;
       }
       if (move) m_ref = mx;
       const float nb = m_ref == -INFINITY ? 0.f : -m_ref;
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      const f2 nb2 = pair(nb, nb);
+      f2 ls[2] = {0, 0};
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        tmem_wait_ld(s[u & 1]);
-        if (u < 3) tmem_ld32_nowait(s_at + (u + 1) * 32, s[(u + 1) & 1]);
+      for (int h = 0; h < 2; ++h) {
         uint32_t p[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          float e0 = fmaf(__uint_as_float(s[u & 1][2 * k]), c, nb), e1 = fmaf(__uint_as_float(s[u & 1][2 * k + 1]), c, nb);
-          if (!whole) {
-            e0 = u * 32 + 2 * k < left ? e0 : -INFINITY;
-            e1 = u * 32 + 2 * k + 1 < left ? e1 : -INFINITY;
-          }
+          float e0, e1;
+          unpair(fma2(pair(__uint_as_float(s[h][2 * k]), __uint_as_float(s[h][2 * k + 1])), c2, nb2), e0, e1);
           const float p0 = exp2_hw(e0), p1 = exp2_hw(e1);
-          ls[k & 3] += p0 + p1;
+          ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
           p[k] = pack16<kQ8>(p0, p1);
         }
-        tmem_st16u(s_at + u * 16, p);   // P of keys 32 u .. over scores read before
+        tmem_st16u(s_at + h * 16, p);   // P of keys 32 h .. over scores read before
       }
-      l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      float l0, l1;
+      unpair(add2(ls[0], ls[1]), l0, l1);
+      l_sum += l0 + l1;
       tmem_wait_st();
       if constexpr (!kQ8) {
         // V rows behind the last key: P is 0 there, V may be anything
@@ -462,11 +464,11 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if ((tid & 31) == 0) mbar_arrive(&p_full[x]);
+      if ((tid & 31) == 0) mbar_arrive(&p_full[u]);
     }
-    const int mine = ntile > x ? (ntile - x + 1) / 2 : 0;   // tiles of the stream
+    // (products complete in order: the last of the other buffer too)
     if (!aborted && mine > 0 &&
-        !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(mine - 1) & 1u, kWait)))
+        !__all_sync(0xffffffffu, mbar_wait(&pv_done[x * 2 + ((mine - 1) & 1)], static_cast<uint32_t>((mine - 1) >> 1) & 1u, kWait)))
       aborted = true;
     if (aborted) {
       *s_abort = 1;
@@ -478,24 +480,24 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       // ------------------------------------------------------------- e4m3 to fp16 --
       const int ct = tid - (kSoftmax + 96), row_of = ct >> 3, ch = ct & 7;   // 16 rows at a time, 16 bytes of one
       for (int j = 0; j < ntile && !aborted; ++j) {
-        const int st = j % 2;
+        const int st = j % W::kRaw;   // (as many tiles of each kind)
 #pragma unroll 1
         for (int v = 0; v < 2; ++v) {   // K, then V
           uint64_t* empty = v ? v_empty : k_empty;
-          const bool ok = !*s_abort && mbar_wait(&raw_full[st], static_cast<uint32_t>(j / 2) & 1u, kWait) &&
-                          (j < 2 || mbar_wait(&empty[st], static_cast<uint32_t>(j / 2 - 1) & 1u, kWait));
+          const bool ok = !*s_abort && mbar_wait(&raw_full[st], static_cast<uint32_t>(j / W::kRaw) & 1u, kWait) &&
+                          (j < W::kRaw || mbar_wait(&empty[st], static_cast<uint32_t>(j / W::kRaw - 1) & 1u, kWait));
           if (!__all_sync(0xffffffffu, ok)) {
             aborted = true;
             break;
           }
           const uint8_t* src = sRaw + (st * 2 + v) * kRawBytes + ch * 16;
           uint8_t* dst = (v ? sV : sK) + st * kTileBytes + (ch >> 2) * kBoxBytes;
-          const int live = v ? kv_end - (t_lo + j) * kTile : kTile;   // V rows behind the last key: zeros
+          const int live = s_bad[st] ? 0 : v ? kv_end - (t_lo + j) * kTile : kTile;   // V rows behind the last key: zeros
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
+          for (int u = 0; u < 4; ++u) {
             const int row = u * 16 + row_of;
             uint4 w = *reinterpret_cast<const uint4*>(src + row * 128);
-            if (row >= live || s_bad[st * 2 + (u >> 2)]) w = make_uint4(0, 0, 0, 0);
+            if (row >= live) w = make_uint4(0, 0, 0, 0);
             uint4 h[2];
             halves_of(w.x, h[0].x, h[0].y);
             halves_of(w.y, h[0].z, h[0].w);
@@ -525,12 +527,12 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   // ------------------------------------------------------- the streams' partials --
   __syncthreads();   // every product is done; loads too, unless a wait ran out
   if (load_thr && *s_abort) {   // the copies still in flight land before the rings are overlaid
-    for (int t = max(0, n_issued - 3); t < n_issued; ++t) {
+    for (int t = max(0, n_issued - W::kK); t < n_issued; ++t) {
       if constexpr (kQ8) {
-        mbar_wait(&raw_full[t % 2], static_cast<uint32_t>(t / 2) & 1u, kWait);
+        mbar_wait(&raw_full[t % W::kRaw], static_cast<uint32_t>(t / W::kRaw) & 1u, kWait);
       } else {
-        mbar_wait(&k_full[t % 3], static_cast<uint32_t>(t / 3) & 1u, kWait);
-        mbar_wait(&v_full[t % 3], static_cast<uint32_t>(t / 3) & 1u, kWait);
+        mbar_wait(&k_full[t % W::kK], static_cast<uint32_t>(t / W::kK) & 1u, kWait);
+        mbar_wait(&v_full[t % W::kV], static_cast<uint32_t>(t / W::kV) & 1u, kWait);
       }
     }
   }
@@ -647,7 +649,7 @@ WideKernel wide_kernel(int share) {
 }
 int bytes_of(int share) { return share ? wide_bytes<__nv_bfloat16>() : wide_bytes<__nv_fp8_storage_t>(); }
 int threads_of(int share) { return share ? Wide<__nv_bfloat16>::kThreads : Wide<__nv_fp8_storage_t>::kThreads; }
-static_assert(kQBytes + 4 * kTileBytes >= (128 * 128 + 256) * 4, "the partials overlay Q and the rings");
+static_assert(kQBytes + 8 * kTileBytes >= (128 * 128 + 256) * 4, "the partials overlay Q and the rings");
 
 // Clusters of S CTAs that can be resident at once (asked once per device and S).
 cudaError_t wide_capacity(int share, int S, int sms, int* n) {
@@ -690,13 +692,13 @@ cudaError_t attn_wide_plan(int batch, int max_len, int sms, AttnWideArgs& a) {
   a.rows = (all + a.q_tiles - 1) / a.q_tiles;
   const long long units = static_cast<long long>(batch) * a.q_tiles * a.Hkv;
   const int tiles = (max_len + kTile - 1) / kTile;
-  // The fewest rounds of resident clusters times a round's length, a tile 1 and the rest of a CTA 8
+  // The fewest rounds of resident clusters times a round's length, a tile 1 and the rest of a CTA 16
   double best = 0;
   for (int S = 1; S <= 8 && S <= tiles; ++S) {
     int cap = 1;
     const cudaError_t e = wide_capacity(a.share, S, sms, &cap);
     if (e != cudaSuccess) return e;
-    const double cost = static_cast<double>((units + cap - 1) / cap) * ((tiles + S - 1) / S + 8.0);
+    const double cost = static_cast<double>((units + cap - 1) / cap) * ((tiles + S - 1) / S + 16.0);
     if (S == 1 || cost < best) {
       best = cost;
       a.S = S;
