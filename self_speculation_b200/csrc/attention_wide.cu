@@ -15,8 +15,9 @@
 // over the cluster's distributed shared memory, in a fixed order.
 //
 // bf16: K and V come by TMA into rings of six pages.  e4m3: a page's K (or V) rows of a kv head are 8 KB in a
-// row and come by bulk copies; four warps turn them into fp16 tiles (exact), four of K and four of V, in the
-// swizzled layout of the descriptors.  K's place frees when S is done, V's when O is.  Q's rows are scaled by a power
+// row and come by bulk copies; eight warps (four for K, four for V) turn them into fp16 tiles (exact), four of K and
+// four of V, in the swizzled layout of the descriptors.  (Four warps for both were the bottleneck, 166 us where
+// eight take 103; moving the bits by integer operations instead of the cvt, 141.)  K's place frees when S is done, V's when O is.  Q's rows are scaled by a power
 // of two into fp16's range there, and P is rounded to fp16 (attention_small.cu has the errors); over the bf16
 // cache P is rounded to bf16.  The maximum that exponents refer to moves only when it has grown by 2^8, so O is
 // rarely rescaled; sums, maxima and O are in fp32.
@@ -53,7 +54,7 @@ template <>
 struct Wide<__nv_fp8_storage_t> {
   static constexpr bool kQ8 = true;
   static constexpr int kK = 4, kV = 4, kRaw = 4;
-  static constexpr int kThreads = kSoftmax + 96 + 128;   // and four converting ones
+  static constexpr int kThreads = kSoftmax + 96 + 256;   // and eight converting ones
 };
 template <typename E>
 __host__ __device__ constexpr int wide_bytes() {
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     }
     for (int i = 0; i < W::kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 4);
+      mbar_init(&raw_empty[i], 8);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
@@ -478,12 +479,12 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   } else if constexpr (kQ8) {
     if (tid >= kSoftmax + 96) {
       // ------------------------------------------------------------- e4m3 to fp16 --
-      const int ct = tid - (kSoftmax + 96), row_of = ct >> 3, ch = ct & 7;   // 16 rows at a time, 16 bytes of one
+      // four warps for K, four for V; 16 rows at a time, a thread 16 bytes of one
+      const int ct = (tid - (kSoftmax + 96)) & 127, row_of = ct >> 3, ch = ct & 7;
+      const bool v = tid >= kSoftmax + 96 + 128;
+      uint64_t* const empty = v ? v_empty : k_empty;
       for (int j = 0; j < ntile && !aborted; ++j) {
         const int st = j % W::kRaw;   // (as many tiles of each kind)
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v) {   // K, then V
-          uint64_t* empty = v ? v_empty : k_empty;
           const bool ok = !*s_abort && mbar_wait(&raw_full[st], static_cast<uint32_t>(j / W::kRaw) & 1u, kWait) &&
                           (j < W::kRaw || mbar_wait(&empty[st], static_cast<uint32_t>(j / W::kRaw - 1) & 1u, kWait));
           if (!__all_sync(0xffffffffu, ok)) {
@@ -513,9 +514,8 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
           __syncwarp();
           if ((tid & 31) == 0) {
             mbar_arrive(v ? &v_full[st] : &k_full[st]);
-            if (v) mbar_arrive(&raw_empty[st]);
+            mbar_arrive(&raw_empty[st]);
           }
-        }
       }
       if (aborted) {
         *s_abort = 1;
