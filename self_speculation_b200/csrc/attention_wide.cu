@@ -585,7 +585,8 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
 
-  // the splits' partials: rank q of the cluster finishes rows q, q + S, .., a warp each
+  // the splits' partials: rank q of the cluster finishes rows q, q + S, .., a warp four at a time (one row at a
+  // time, the waits on shared memory of other CTAs and on the prefix's partials were half of a short CTA)
   const int S = a.S;
   if (S > 1) cluster_sync();
   float vscale = 1.f;
@@ -594,49 +595,69 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int d4 = tid & 31;
   const uint32_t o_base = smem_u32(sO), ml_base = smem_u32(sML);
-  for (int rr = rank + warp * S; rr < rows; rr += S * (W::kThreads / 32)) {
-    const uint32_t o_off = (rr * 128 + ((d4 ^ (rr & 31)) << 2)) * 4;
-    float M, L;
-    float4 acc;
-    if (S == 1) {
-      M = sML[2 * rr];
-      L = sML[2 * rr + 1];
-      acc = *reinterpret_cast<const float4*>(reinterpret_cast<const uint8_t*>(sO) + o_off);
-    } else {
-      float2 ml[8];
-      float4 ov[8];
+  constexpr int kRows = 4;
+  for (int t0 = warp * kRows; rank + t0 * S < rows; t0 += W::kThreads / 32 * kRows) {
+    size_t at[kRows];   // token x query head
+    float2 ml[kRows], pre_ml[kRows];
+    float4 acc[kRows], pre[kRows];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        ml[q] = make_float2(-INFINITY, 0.f);
-        ov[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (q < S) {
-          ml[q] = ld_dsmem_f2(dsmem_addr(ml_base, q) + rr * 8);
-          ov[q] = ld_dsmem_f4(dsmem_addr(o_base, q) + o_off);
+    for (int i = 0; i < kRows; ++i) {
+      const int rr = min(rank + (t0 + i) * S, rows - 1);   // (past the end: the last row again, not stored)
+      const int row = r0 + rr, pos = row / a.G;
+      at[i] = (static_cast<size_t>(b) * a.m + pos) * a.Hq + static_cast<size_t>(g) * a.G + (row - pos * a.G);
+      // (max, sum) of split q in lane q
+      ml[i] = d4 < S ? ld_dsmem_f2((S > 1 ? dsmem_addr(ml_base, d4) : ml_base) + rr * 8) : make_float2(-INFINITY, 0.f);
+      if constexpr (kShare == kOwnPass)
+        if (a.part_o != nullptr) {
+          pre_ml[i] = a.part_ml[at[i]];
+          pre[i] = reinterpret_cast<const float4*>(a.part_o)[at[i] * 32 + d4];
+        }
+      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float M[kRows], L[kRows], w[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      M[i] = ml[i].x;
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], off));
+      M[i] = __shfl_sync(0xffffffffu, M[i], 0);
+      w[i] = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - M[i]);
+      L[i] = w[i] * ml[i].y;
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) L[i] += __shfl_xor_sync(0xffffffffu, L[i], off);
+      L[i] = __shfl_sync(0xffffffffu, L[i], 0);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < S) {
+        const uint32_t o_peer = S > 1 ? dsmem_addr(o_base, q) : o_base;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int rr = min(rank + (t0 + i) * S, rows - 1);
+          const float4 v = ld_dsmem_f4(o_peer + (rr * 128 + ((d4 ^ (rr & 31)) << 2)) * 4);
+          const float wq = __shfl_sync(0xffffffffu, w[i], q);
+          if (wq != 0.f) {   // (a split without a key of the row may hold anything)
+            acc[i].x += wq * v.x;
+            acc[i].y += wq * v.y;
+            acc[i].z += wq * v.z;
+            acc[i].w += wq * v.w;
+          }
         }
       }
-      M = -INFINITY;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) M = fmaxf(M, ml[q].x);
-      L = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (ml[q].x != -INFINITY) {
-          const float w = exp2f(ml[q].x - M);
-          L += w * ml[q].y;
-          acc.x += w * ov[q].x;
-          acc.y += w * ov[q].y;
-          acc.z += w * ov[q].z;
-          acc.w += w * ov[q].w;
-        }
+    for (int i = 0; i < kRows; ++i) {
+      if (rank + (t0 + i) * S >= rows) break;
+      if constexpr (kShare == kPrefixPass) {
+        reinterpret_cast<float4*>(a.part_o)[at[i] * 32 + d4] = acc[i];
+        if (d4 == 0) a.part_ml[at[i]] = make_float2(M[i], L[i]);
+        continue;
+      }
+      if constexpr (kShare == kOwnPass)
+        if (a.part_o != nullptr) share_add(pre_ml[i], pre[i], M[i], L[i], acc[i]);
+      const float k = L[i] > 0.f ? vscale / L[i] : 0.f;
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at[i] * 128 + 4 * d4) =
+          make_uint2(pack16<false>(acc[i].x * k, acc[i].y * k), pack16<false>(acc[i].z * k, acc[i].w * k));
     }
-    const int row = r0 + rr, pos = row / a.G;
-    const size_t at = (static_cast<size_t>(b) * a.m + pos) * a.Hq + static_cast<size_t>(g) * a.G + (row - pos * a.G);
-    if constexpr (kShare != 0)
-      if (share_merge<kShare>(a.part_o, a.part_ml, at, d4, M, L, acc)) continue;
-    const float k = L > 0.f ? vscale / L : 0.f;
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * 128 + 4 * d4) =
-        make_uint2(pack16<false>(acc.x * k, acc.y * k), pack16<false>(acc.z * k, acc.w * k));
   }
   if (S > 1) cluster_sync();   // peers may still be reading this CTA's shared memory
 }
