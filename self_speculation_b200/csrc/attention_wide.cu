@@ -8,10 +8,11 @@
 // cycles of tensor core (S = Q K^T and O += P V, 128 x 128 x 128 each) and as many of the exponential
 // unit (16 a cycle and SM), so the two have to run side by side: the even and the odd pages are two
 // streams, each with its own S, O, running max and sum, its own four softmax warps (a thread per row) and its
-// own issuing thread.  A stream has two S buffers: the scores of its next page are there when the softmax is
-// done with one, and O += P V runs behind (P is written over its S, in 16 bits).  That fills tensor memory: 4 x 64
-// columns of S, 2 x 128 of O.  With one S of 128 keys a stream, a stream waited 2400 of 6000 cycles a
-// tile for P V and then S.  The streams' partials meet in shared memory at the end, those of the KV splits
+// own issuing thread.  A softmax thread takes its row's 64 scores into registers at once, so S of the stream's
+// next page is issued right then and is there when the softmax is done; P (in 16 bits) goes beside it, and O += P V
+// runs behind.  That fills tensor memory: 64 columns of S and 32 of P a stream, 128 of O, and 64 of Q.  Q is there
+// because shared memory is the next bound: a page's K and V cross it twice (256 cycles in, 256 out to the tensor
+// core), and 512 more if Q had to be read for every S.  The streams' partials meet in shared memory at the end, those of the KV splits
 // over the cluster's distributed shared memory, in a fixed order.
 //
 // bf16: K and V come by TMA into rings of six pages.  e4m3: a page's K (or V) rows of a kv head are 8 KB in a
@@ -31,6 +32,10 @@
 #include "attn_share.cuh"
 #include "common.cuh"
 
+#ifndef FMAB
+#define FMAB 0
+#define FMAQ 0
+#endif
 namespace nld {
 
 namespace {
@@ -39,7 +44,6 @@ constexpr int kTile = kPage;                 // keys of a tile
 constexpr int kTileBytes = kTile * 256;      // K (or V) of a tile in 16 bits: [2 boxes of 64 dims][64 keys][128 B]
 constexpr int kBoxBytes = kTileBytes / 2;
 constexpr int kRawBytes = kTile * 128;       // the same in e4m3: [64 keys][128 B]
-constexpr int kQBytes = 128 * 256;           // [2 boxes][128 rows][128 B]
 constexpr int kSoftmax = 256;                // threads: two streams of 128, a row each
 constexpr float kMove = 8.f;                 // log2 units
 constexpr uint64_t kWait = 2000000000ull;
@@ -48,17 +52,19 @@ template <typename E>
 struct Wide {   // bf16
   static constexpr bool kQ8 = false;
   static constexpr int kK = 6, kV = 6, kRaw = 0;        // tiles of K, of V, raw ones
+  static constexpr int kFma = FMAB;                        // of 16 exponentials, those on the multiply-add pipe
   static constexpr int kThreads = kSoftmax + 96;        // two issuing warps, a loading one
 };
 template <>
 struct Wide<__nv_fp8_storage_t> {
   static constexpr bool kQ8 = true;
   static constexpr int kK = 4, kV = 4, kRaw = 4;
+  static constexpr int kFma = FMAQ;
   static constexpr int kThreads = kSoftmax + 96 + 256;   // and eight converting ones
 };
 template <typename E>
 __host__ __device__ constexpr int wide_bytes() {
-  return 1024 + kQBytes + (Wide<E>::kK + Wide<E>::kV) * kTileBytes + Wide<E>::kRaw * 2 * kRawBytes + 512;
+  return 1024 + (Wide<E>::kK + Wide<E>::kV) * kTileBytes + Wide<E>::kRaw * 2 * kRawBytes + 512;
 }
 
 NLD_DEV void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -124,6 +130,26 @@ NLD_DEV f2 fma2(f2 a, f2 b, f2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+NLD_DEV f2 both(float a) { return pair(a, a); }
+// 2^x of two numbers on the multiply-add pipe, relative error 2^-23: x = n + f, |f| <= 1/2, by adding 1.5 2^23; 2^f
+// by its Chebyshev interpolant of degree 5; n into the exponent.  x under -126 counts as -126, x <= 126.
+NLD_DEV void exp2_fma(f2 x, float& y0, float& y1) {
+  float a, b;
+  unpair(x, a, b);
+  x = pair(fmaxf(a, -126.f), fmaxf(b, -126.f));
+  const f2 t = add2(x, both(12582912.f));
+  const f2 f = fma2(add2(t, both(-12582912.f)), both(-1.f), x);
+  f2 p = fma2(f, both(0.001339086336f), both(0.009676031918f));
+  p = fma2(f, p, both(0.05550357114f));
+  p = fma2(f, p, both(0.2402210749f));
+  p = fma2(f, p, both(0.693147188f));
+  p = fma2(f, p, both(1.f));
+  float t0, t1;
+  unpair(t, t0, t1);
+  unpair(p, a, b);
+  y0 = __uint_as_float(__float_as_uint(a) + (__float_as_uint(t0) << 23));
+  y1 = __uint_as_float(__float_as_uint(b) + (__float_as_uint(t1) << 23));
+}
 template <bool kHalf>
 NLD_DEV uint32_t pack16(float lo, float hi) {
   if constexpr (kHalf) {
@@ -146,6 +172,12 @@ NLD_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar
                : "memory");
 }
 
+// Columns of tensor memory.
+NLD_DEV constexpr uint32_t s_col_of(int stream) { return stream * 96; }
+NLD_DEV constexpr uint32_t p_col_of(int stream) { return stream * 96 + 64; }
+NLD_DEV constexpr uint32_t o_col_of(int stream) { return 192 + stream * 128; }
+constexpr uint32_t kQCol = 448;
+
 template <typename E, int kShare>
 __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     attn_wide_kernel(const __grid_constant__ CUtensorMap tmKV, const AttnWideArgs a) {
@@ -153,8 +185,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   constexpr bool kQ8 = W::kQ8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* sQ = smem;
-  uint8_t* sK = sQ + kQBytes;                  // [kK] tiles
+  uint8_t* sK = smem;                          // [kK] tiles
   uint8_t* sV = sK + W::kK * kTileBytes;       // [kV]
   uint8_t* sRaw = sV + W::kV * kTileBytes;     // [kRaw][K, V]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sRaw + W::kRaw * 2 * kRawBytes);
@@ -164,9 +195,10 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   uint64_t* v_empty = bars + 18;       // [kV] O += P V of the tile done
   uint64_t* raw_full = bars + 24;      // [kRaw] bytes landed
   uint64_t* raw_empty = bars + 28;     // [kRaw] converted
-  uint64_t* s_full = bars + 32;        // [stream][buffer] S written
-  uint64_t* p_full = bars + 36;        // [stream][buffer] P written
-  uint64_t* pv_done = bars + 40;       // [stream][buffer] O += P V done
+  uint64_t* s_full = bars + 32;        // [stream] S written
+  uint64_t* s_read = bars + 34;        // [stream] S in registers
+  uint64_t* p_full = bars + 36;        // [stream] P written
+  uint64_t* pv_done = bars + 38;       // [stream] O += P V done
   uint64_t* fin = bars + 44;           // every product done
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 45);
   volatile int* s_abort = reinterpret_cast<volatile int*>(bars + 46);
@@ -194,8 +226,11 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 8);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_read[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
@@ -205,7 +240,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     if constexpr (!kQ8) tma_prefetch_desc(&tmKV);
   }
   if (warp == kSoftmax / 32) {
-    tmem_alloc(s_tmem, 512);   // S of the streams, O of the streams
+    tmem_alloc(s_tmem, 512);   // S and P of the streams, O of the streams, Q
     tmem_relinquish();
   }
 
@@ -228,7 +263,12 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   const int t_lo = split * per;
   const int ntile = max(0, min(n_pages, t_lo + per) - t_lo);
 
-  // Q into shared memory, K-major in 128-byte-swizzled boxes: thread (stream x, row r) writes box x of row r
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  // Q into tensor memory, two dims a column: thread (stream x, row r) writes dims 64 x .. of row r
   const int x = tid >> 7, r = tid & 127;   // softmax threads
   float c = a.scale_log2;                  // the scores' scale to log2 units
   if (softmax_thr) {
@@ -236,43 +276,44 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     const uint4* src = reinterpret_cast<const uint4*>(
         static_cast<const __nv_bfloat16*>(a.q) +
         ((static_cast<size_t>(b) * a.m + (r < rows ? pos : 0)) * a.Hq + static_cast<size_t>(g) * a.G + (r < rows ? row - pos * a.G : 0)) * 128);
-    float down = 1.f;
+    uint4 v[8];   // dims 64 x ..
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = r < rows ? src[8 * x + i] : make_uint4(0, 0, 0, 0);
     if constexpr (kQ8) {
       float big = 0.f;
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const uint4 v = src[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+      for (int i = 0; i < 8; ++i) {
+        const uint4 o = src[8 * (1 - x) + i];   // the row's other half, for its largest element
+        const uint32_t w[8] = {v[i].x, v[i].y, v[i].z, v[i].w, o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
       }
       // 2^-e brings the largest element into [1, 2); zero, subnormal and infinite rows keep e in range
       const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -126), 126);
       const float ks = a.k_scale[g];
-      down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), ks);   // (the scores' scale stays positive)
+      const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), ks);   // (the scores' scale stays positive)
       c = fabsf(ks) * a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        v = src[8 * x + i];
-        if constexpr (kQ8) {
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int i = 0; i < 8; ++i) {
+        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack16<true>(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xffff0000u) * down);
-          v = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int q = 0; q < 4; ++q)
+          w[q] = pack16<true>(__uint_as_float(w[q] << 16) * down, __uint_as_float(w[q] & 0xffff0000u) * down);
+        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      *reinterpret_cast<uint4*>(sQ + x * (kQBytes / 2) + r * 128 + ((i ^ (r & 7)) << 4)) = v;
     }
-    fence_proxy_async();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w[16] = {v[4 * h].x, v[4 * h].y, v[4 * h].z, v[4 * h].w, v[4 * h + 1].x, v[4 * h + 1].y, v[4 * h + 1].z,
+                              v[4 * h + 1].w, v[4 * h + 2].x, v[4 * h + 2].y, v[4 * h + 2].z, v[4 * h + 2].w, v[4 * h + 3].x,
+                              v[4 * h + 3].y, v[4 * h + 3].z, v[4 * h + 3].w};
+      tmem_st16u(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kQCol + x * 32 + h * 16, w);
+    }
+    tmem_wait_st();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
   if constexpr (kShare == kPrefixPass) pdl_launch_dependents();
 
   bool aborted = false;
@@ -332,29 +373,33 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     constexpr uint32_t kKind = kQ8 ? (1u << 4) : (1u << 4) | (1u << 7) | (1u << 10);   // fp32 accumulator; fp16 or bf16
     constexpr uint32_t idS = kKind | ((static_cast<uint32_t>(kTile) >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t idO = kKind | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);   // B (V) MN-major
-    const uint32_t o_col = tmem + 256 + y * 128;
     const int mine = ntile > y ? (ntile - y + 1) / 2 : 0;   // tiles of the stream
-    // S of the stream's tile i into buffer i & 1, free once O += P V of tile i - 2 has read P there
+    const uint32_t s_col = tmem + s_col_of(y), p_col = tmem + p_col_of(y), o_col = tmem + o_col_of(y);
+    // S of the stream's tile i, once the softmax has read that of tile i - 1
     auto s_step = [&](int i) -> bool {
-      const int j = y + 2 * i, ks = j % W::kK, u = y * 2 + (i & 1);
+      const int j = y + 2 * i, ks = j % W::kK;
       if (*s_abort || !mbar_wait(&k_full[ks], static_cast<uint32_t>(j / W::kK) & 1u, kWait) ||
-          (i >= 2 && !mbar_wait(&pv_done[u], static_cast<uint32_t>((i - 2) >> 1) & 1u, kWait)))
+          (i >= 1 && !mbar_wait(&s_read[y], static_cast<uint32_t>(i - 1) & 1u, kWait)))
         return false;
       tc_fence_after();
 #pragma unroll
       for (int box = 0; box < 2; ++box)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          tc_mma_f16(tmem + u * kTile, sdesc_k_sw128(smem_u32(sQ + box * (kQBytes / 2))) + 2 * kk,
-                     sdesc_k_sw128(smem_u32(sK + ks * kTileBytes + box * kBoxBytes)) + 2 * kk, idS, (box > 0 || kk > 0) ? 1u : 0u);
+          tc_mma_ts(s_col, tmem + kQCol + (box * 4 + kk) * 8, sdesc_k_sw128(smem_u32(sK + ks * kTileBytes + box * kBoxBytes)) + 2 * kk,
+                    idS, (box > 0 || kk > 0) ? 1u : 0u);
       tc_commit(&k_empty[ks]);
-      tc_commit(&s_full[u]);
+      tc_commit(&s_full[y]);
       return true;
     };
-    for (int i = 0; i < min(2, mine) && !aborted; ++i) aborted = !s_step(i);
+    if (mine > 0) aborted = !s_step(0);
     for (int i = 0; i < mine && !aborted; ++i) {
-      const int j = y + 2 * i, vs = j % W::kV, u = y * 2 + (i & 1);
-      if (*s_abort || !mbar_wait(&p_full[u], static_cast<uint32_t>(i >> 1) & 1u, kWait) ||
+      const int j = y + 2 * i, vs = j % W::kV;
+      if (i + 1 < mine && !s_step(i + 1)) {
+        aborted = true;
+        break;
+      }
+      if (*s_abort || !mbar_wait(&p_full[y], static_cast<uint32_t>(i) & 1u, kWait) ||
           !mbar_wait(&v_full[vs], static_cast<uint32_t>(j / W::kV) & 1u, kWait)) {
         aborted = true;
         break;
@@ -362,11 +407,10 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)   // 16 keys: 8 columns of P
-        tc_mma_ts(o_col, tmem + u * kTile + k * 8, desc_mn(smem_u32(sV + vs * kTileBytes + k * 2048), kBoxBytes, 1024), idO,
+        tc_mma_ts(o_col, p_col + k * 8, desc_mn(smem_u32(sV + vs * kTileBytes + k * 2048), kBoxBytes, 1024), idO,
                   (i > 0 || k > 0) ? 1u : 0u);
       tc_commit(&v_empty[vs]);
-      tc_commit(&pv_done[u]);
-      if (i + 2 < mine) aborted = !s_step(i + 2);
+      tc_commit(&pv_done[y]);
     }
     if (aborted) {
       *s_abort = 1;
@@ -379,14 +423,13 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     // ----------------------------------------------------------- softmax of stream x, row r --
     const int seen = r < rows ? seen_by(r0 + r) : 0;
     const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t o_at = tmem + lane + 256 + x * 128;
+    const uint32_t s_at = tmem + lane + s_col_of(x), p_at = tmem + lane + p_col_of(x), o_at = tmem + lane + o_col_of(x);
     const f2 c2 = pair(c, c);
     const int mine = ntile > x ? (ntile - x + 1) / 2 : 0;   // tiles of the stream
     for (int i = 0; i < mine; ++i) {
-      const int j = x + 2 * i, u = x * 2 + (i & 1);
-      const uint32_t s_at = tmem + lane + u * kTile;
+      const int j = x + 2 * i;
       // tcgen05.ld / st are for whole warps: every exit of this loop is taken by the warp together
-      if (!__all_sync(0xffffffffu, !*s_abort && mbar_wait(&s_full[u], static_cast<uint32_t>(i >> 1) & 1u, kWait))) {
+      if (!__all_sync(0xffffffffu, !*s_abort && mbar_wait(&s_full[x], static_cast<uint32_t>(i) & 1u, kWait))) {
         aborted = true;
         break;
       }
@@ -396,6 +439,9 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       tmem_ld32_nowait(s_at + 32, s[1]);
       tmem_wait_ld(s[0]);
       tmem_wait_ld(s[1]);
+      tc_fence_before();
+      __syncwarp();
+      if ((tid & 31) == 0) mbar_arrive(&s_read[x]);
       const int left = seen - (t_lo + j) * kTile;   // keys of the tile that the row sees
       if (!__all_sync(0xffffffffu, left >= kTile)) {
 #pragma unroll
@@ -409,7 +455,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       const bool move = mx > m_ref + kMove;
       const bool scale_o = move && m_ref != -INFINITY;
       if (__any_sync(0xffffffffu, scale_o)) {   // (i > 0: m_ref was set)
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[u ^ 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, kWait))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(i - 1) & 1u, kWait))) {
           aborted = true;
           break;
         }
@@ -431,19 +477,32 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       const float nb = m_ref == -INFINITY ? 0.f : -m_ref;
       const f2 nb2 = pair(nb, nb);
       f2 ls[2] = {0, 0};
+      uint32_t p[2][16];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t p[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          float e0, e1;
-          unpair(fma2(pair(__uint_as_float(s[h][2 * k]), __uint_as_float(s[h][2 * k + 1])), c2, nb2), e0, e1);
-          const float p0 = exp2_hw(e0), p1 = exp2_hw(e1);
+          const f2 e2 = fma2(pair(__uint_as_float(s[h][2 * k]), __uint_as_float(s[h][2 * k + 1])), c2, nb2);
+          float p0, p1;
+          if (k % 16 >= 16 - W::kFma) {
+            exp2_fma(e2, p0, p1);
+          } else {
+            unpair(e2, p0, p1);
+            p0 = exp2_hw(p0);
+            p1 = exp2_hw(p1);
+          }
           ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
-          p[k] = pack16<kQ8>(p0, p1);
+          p[h][k] = pack16<kQ8>(p0, p1);
         }
-        tmem_st16u(s_at + h * 16, p);   // P of keys 32 h .. over scores read before
       }
+      // P is free once O += P V of the tile before has read it
+      if (i >= 1 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(i - 1) & 1u, kWait))) {
+        aborted = true;
+        break;
+      }
+      tc_fence_after();
+      tmem_st16u(p_at, p[0]);
+      tmem_st16u(p_at + 16, p[1]);
       float l0, l1;
       unpair(add2(ls[0], ls[1]), l0, l1);
       l_sum += l0 + l1;
@@ -465,11 +524,9 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if ((tid & 31) == 0) mbar_arrive(&p_full[u]);
+      if ((tid & 31) == 0) mbar_arrive(&p_full[x]);
     }
-    // (products complete in order: the last of the other buffer too)
-    if (!aborted && mine > 0 &&
-        !__all_sync(0xffffffffu, mbar_wait(&pv_done[x * 2 + ((mine - 1) & 1)], static_cast<uint32_t>((mine - 1) >> 1) & 1u, kWait)))
+    if (!aborted && mine > 0 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(mine - 1) & 1u, kWait)))
       aborted = true;
     if (aborted) {
       *s_abort = 1;
@@ -540,7 +597,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   float* sO = reinterpret_cast<float*>(smem);   // [128][128]; float4 s of row r at s ^ (r % 32)
   float* sML = sO + 128 * 128;                  // [128][2] max, sum
   const bool have = softmax_thr && ntile > x && !*s_abort;
-  const uint32_t o_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 + x * 128;
+  const uint32_t o_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + o_col_of(x & 1);
   // stream 0 leaves its row, stream 1 adds its own
   auto leave = [&](bool add) {
     float w0 = 0.f, w1 = have ? 1.f : 0.f, M = have ? m_ref : -INFINITY, L = have ? l_sum : 0.f;
@@ -670,7 +727,7 @@ WideKernel wide_kernel(int share) {
 }
 int bytes_of(int share) { return share ? wide_bytes<__nv_bfloat16>() : wide_bytes<__nv_fp8_storage_t>(); }
 int threads_of(int share) { return share ? Wide<__nv_bfloat16>::kThreads : Wide<__nv_fp8_storage_t>::kThreads; }
-static_assert(kQBytes + 8 * kTileBytes >= (128 * 128 + 256) * 4, "the partials overlay Q and the rings");
+static_assert(8 * kTileBytes >= (128 * 128 + 256) * 4, "the partials overlay the rings");
 
 // Clusters of S CTAs that can be resident at once (asked once per device and S).
 cudaError_t wide_capacity(int share, int S, int sms, int* n) {
