@@ -166,6 +166,14 @@ NLD_DEV void halves_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
+// The whole warp's wait: the same answer for every lane.
+NLD_DEV bool warp_wait(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWait)); }
+// One lane of the (converged) warp.
+NLD_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
 NLD_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
@@ -204,13 +212,13 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(bars + 46);
   int* s_bad = reinterpret_cast<int*>(bars + 47);   // [kRaw] the page is outside the pool
 
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform for the compiler too)
   const int split = blockIdx.x, g = blockIdx.y;
   const int b = blockIdx.z / a.q_tiles, qt = blockIdx.z - b * a.q_tiles;
   const int all = a.m * a.G;                              // rows of the (sequence, kv head)
   const int r0 = qt * a.rows, rows = min(a.rows, all - r0);   // of this CTA
   const bool softmax_thr = tid < kSoftmax;
-  const bool issue_thr = tid == kSoftmax || tid == kSoftmax + 32;
+  const bool issue_warp = warp == kSoftmax / 32 || warp == kSoftmax / 32 + 1;
   const bool load_thr = tid == kSoftmax + 64;
 
   if (tid == 0) {
@@ -328,7 +336,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       if (bad) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
       if constexpr (kQ8) {
         const int st = j % W::kRaw;
-        if (j >= W::kRaw && (*s_abort || !mbar_wait(&raw_empty[st], static_cast<uint32_t>(j / W::kRaw - 1) & 1u, kWait))) {
+        if (j >= W::kRaw && (!mbar_wait(&raw_empty[st], static_cast<uint32_t>(j / W::kRaw - 1) & 1u, kWait))) {
           aborted = true;
           break;
         }
@@ -340,7 +348,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
         bulk_load(sRaw + (st * 2 + 1) * kRawBytes, kp + static_cast<size_t>(a.Hkv) * kRawBytes, kRawBytes, &raw_full[st]);
       } else {
         const int st = j % W::kK;
-        if (j >= W::kK && (*s_abort || !mbar_wait(&k_empty[st], static_cast<uint32_t>(j / W::kK - 1) & 1u, kWait))) {
+        if (j >= W::kK && (!mbar_wait(&k_empty[st], static_cast<uint32_t>(j / W::kK - 1) & 1u, kWait))) {
           aborted = true;
           break;
         }
@@ -350,7 +358,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
         for (int box = 0; box < 2; ++box)
           tma_load_2d(sK + st * kTileBytes + box * kBoxBytes, &tmKV, &k_full[st], box * 64,
                       bad ? -kPage : (page * 2 * a.Hkv + g) * kPage);
-        if (j >= W::kV && (*s_abort || !mbar_wait(&v_empty[st], static_cast<uint32_t>(j / W::kV - 1) & 1u, kWait))) {
+        if (j >= W::kV && (!mbar_wait(&v_empty[st], static_cast<uint32_t>(j / W::kV - 1) & 1u, kWait))) {
           mbar_wait(&k_full[st], static_cast<uint32_t>(j / W::kK) & 1u, kWait);   // the copies in flight land
           aborted = true;
           break;
@@ -367,58 +375,73 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       *s_abort = 1;
       set_err(a.err, NLD_DEVERR_TIMEOUT);
     }
-  } else if (issue_thr) {
+  } else if (issue_warp) {
     // ------------------------------------------- products of stream y: tiles y, y + 2, .. --
-    const int y = tid == kSoftmax ? 0 : 1;
+    // The whole warp walks the loop and one lane issues: the operands of tcgen05.mma are uniform registers, and with
+    // a single thread in here each one was moved there anew, 480 cycles for the four products of P V.
+    const int y = warp - kSoftmax / 32;
+    const bool leader = elect_one();   // the same lane throughout: a commit counts the issuing thread's products
     constexpr uint32_t kKind = kQ8 ? (1u << 4) : (1u << 4) | (1u << 7) | (1u << 10);   // fp32 accumulator; fp16 or bf16
     constexpr uint32_t idS = kKind | ((static_cast<uint32_t>(kTile) >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t idO = kKind | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);   // B (V) MN-major
     const int mine = ntile > y ? (ntile - y + 1) / 2 : 0;   // tiles of the stream
     const uint32_t s_col = tmem + s_col_of(y), p_col = tmem + p_col_of(y), o_col = tmem + o_col_of(y);
+    const uint64_t k_desc = sdesc_k_sw128(smem_u32(sK)), v_desc = desc_mn(smem_u32(sV), kBoxBytes, 1024);
+    int ks = y, kp = 0, vs = y, vp = 0;   // stage and parity of the stream's next K and V
     // S of the stream's tile i, once the softmax has read that of tile i - 1
     auto s_step = [&](int i) -> bool {
-      const int j = y + 2 * i, ks = j % W::kK;
-      if (*s_abort || !mbar_wait(&k_full[ks], static_cast<uint32_t>(j / W::kK) & 1u, kWait) ||
-          (i >= 1 && !mbar_wait(&s_read[y], static_cast<uint32_t>(i - 1) & 1u, kWait)))
-        return false;
+      if (!warp_wait(&k_full[ks], kp) || (i >= 1 && !warp_wait(&s_read[y], static_cast<uint32_t>(i - 1) & 1u))) return false;
       tc_fence_after();
+      const uint64_t d = k_desc + ks * (kTileBytes >> 4);
+      if (leader) {
 #pragma unroll
-      for (int box = 0; box < 2; ++box)
+        for (int box = 0; box < 2; ++box)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_ts(s_col, tmem + kQCol + (box * 4 + kk) * 8, sdesc_k_sw128(smem_u32(sK + ks * kTileBytes + box * kBoxBytes)) + 2 * kk,
-                    idS, (box > 0 || kk > 0) ? 1u : 0u);
-      tc_commit(&k_empty[ks]);
-      tc_commit(&s_full[y]);
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_ts(s_col, tmem + kQCol + (box * 4 + kk) * 8, d + box * (kBoxBytes >> 4) + 2 * kk, idS, (box > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(&k_empty[ks]);
+        tc_commit(&s_full[y]);
+      }
+      __syncwarp();
+      ks += 2;
+      if (ks >= W::kK) {
+        ks -= W::kK;
+        kp ^= 1;
+      }
       return true;
     };
     if (mine > 0) aborted = !s_step(0);
     for (int i = 0; i < mine && !aborted; ++i) {
-      const int j = y + 2 * i, vs = j % W::kV;
-      if (i + 1 < mine && !s_step(i + 1)) {
-        aborted = true;
-        break;
-      }
-      if (*s_abort || !mbar_wait(&p_full[y], static_cast<uint32_t>(i) & 1u, kWait) ||
-          !mbar_wait(&v_full[vs], static_cast<uint32_t>(j / W::kV) & 1u, kWait)) {
+      if ((i + 1 < mine && !s_step(i + 1)) || !warp_wait(&p_full[y], static_cast<uint32_t>(i) & 1u) || !warp_wait(&v_full[vs], vp)) {
         aborted = true;
         break;
       }
       tc_fence_after();
+      const uint64_t d = v_desc + vs * (kTileBytes >> 4);
+      if (leader) {
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)   // 16 keys: 8 columns of P
-        tc_mma_ts(o_col, p_col + k * 8, desc_mn(smem_u32(sV + vs * kTileBytes + k * 2048), kBoxBytes, 1024), idO,
-                  (i > 0 || k > 0) ? 1u : 0u);
-      tc_commit(&v_empty[vs]);
-      tc_commit(&pv_done[y]);
+        for (int k = 0; k < kTile / 16; ++k)   // 16 keys: 8 columns of P
+          tc_mma_ts(o_col, p_col + k * 8, d + k * (2048 >> 4), idO, (i > 0 || k > 0) ? 1u : 0u);
+        tc_commit(&v_empty[vs]);
+        tc_commit(&pv_done[y]);
+      }
+      __syncwarp();
+      vs += 2;
+      if (vs >= W::kV) {
+        vs -= W::kV;
+        vp ^= 1;
+      }
     }
-    if (aborted) {
+    if (aborted && leader) {
       *s_abort = 1;
       set_err(a.err, NLD_DEVERR_TIMEOUT);
     }
-    // every product of this thread is done before tensor memory is released
-    tc_commit(fin);
-    mbar_wait(fin, 0, kWait);
+    // every product of this warp is done before tensor memory is released
+    if (leader) {
+      tc_commit(fin);
+      mbar_wait(fin, 0, kWait);
+    }
+    __syncwarp();
   } else if (softmax_thr) {
     // ----------------------------------------------------------- softmax of stream x, row r --
     const int seen = r < rows ? seen_by(r0 + r) : 0;
@@ -429,7 +452,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     for (int i = 0; i < mine; ++i) {
       const int j = x + 2 * i;
       // tcgen05.ld / st are for whole warps: every exit of this loop is taken by the warp together
-      if (!__all_sync(0xffffffffu, !*s_abort && mbar_wait(&s_full[x], static_cast<uint32_t>(i) & 1u, kWait))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], static_cast<uint32_t>(i) & 1u, kWait))) {
         aborted = true;
         break;
       }
@@ -542,7 +565,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       uint64_t* const empty = v ? v_empty : k_empty;
       for (int j = 0; j < ntile && !aborted; ++j) {
         const int st = j % W::kRaw;   // (as many tiles of each kind)
-          const bool ok = !*s_abort && mbar_wait(&raw_full[st], static_cast<uint32_t>(j / W::kRaw) & 1u, kWait) &&
+          const bool ok = mbar_wait(&raw_full[st], static_cast<uint32_t>(j / W::kRaw) & 1u, kWait) &&
                           (j < W::kRaw || mbar_wait(&empty[st], static_cast<uint32_t>(j / W::kRaw - 1) & 1u, kWait));
           if (!__all_sync(0xffffffffu, ok)) {
             aborted = true;
