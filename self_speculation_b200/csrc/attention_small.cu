@@ -517,9 +517,10 @@ void attn_small_plan(int batch, int max_len, int sms, AttnSmallArgs& a) {
   a.r_tiles = (rows + 16 * a.mt - 1) / (16 * a.mt);
   const int pages = (max_len + kPage - 1) / kPage;
   const long long units = static_cast<long long>(batch) * a.r_tiles * a.Hkv;
-  // splits until every SM holds its three CTAs twice, of a page per key group at least
+  // splits until every SM holds its three CTAs twice, of a page per key group at least; once beside a prefix, where a
+  // sequence's own keys are few (64 sequences of up to 512 keys under one of 16384: 63 -> 55 us for both passes)
   const int kw = kWarps / a.mt;
-  long long S = (6LL * sms + units - 1) / units;
+  long long S = ((a.share == kOwnPass ? 3LL : 6LL) * sms + units - 1) / units;
   S = std::min<long long>(std::min<long long>(S, 8), std::max(1, pages / kw));
   a.S = static_cast<int>(std::max<long long>(1, S));
 }

@@ -12,15 +12,21 @@
 // next page is issued right then and is there when the softmax is done; P (in 16 bits) goes beside it, and O += P V
 // runs behind.  That fills tensor memory: 64 columns of S and 32 of P a stream, 128 of O, and 64 of Q.  Q is there
 // because shared memory is the next bound: a page's K and V cross it twice (256 cycles in, 256 out to the tensor
-// core), and 512 more if Q had to be read for every S.  The streams' partials meet in shared memory at the end, those of the KV splits
-// over the cluster's distributed shared memory, in a fixed order.
+// core), and 512 more if Q had to be read for every S.  The streams' partials meet in shared memory at the end,
+// those of the KV splits over the cluster's distributed shared memory, in a fixed order.
+//
+// What it measured: two pages of 128 rows take 1850 cycles, 55 % of the exponential unit; the rest is the latency of a
+// softmax thread's steps (scores in 85 cycles, maximum 175, exponentials 512 to 800, waits 370, P out 100).  Two threads a
+// row (sixteen softmax warps) took 10 to 17 % longer, a quarter of the exponentials as polynomials on the multiply-add
+// pipe 1 to 6 %, the maximum taken beside the exponentials of a stale one the same time.  A CTA's fixed cost is 9 us
+// (Q 2, partials 2, merge 3.5), which few pages a CTA do not hide.
 //
 // bf16: K and V come by TMA into rings of six pages.  e4m3: a page's K (or V) rows of a kv head are 8 KB in a
 // row and come by bulk copies; eight warps (four for K, four for V) turn them into fp16 tiles (exact), four of K and
 // four of V, in the swizzled layout of the descriptors.  (Four warps for both were the bottleneck, 166 us where
-// eight take 103; moving the bits by integer operations instead of the cvt, 141.)  K's place frees when S is done, V's when O is.  Q's rows are scaled by a power
-// of two into fp16's range there, and P is rounded to fp16 (attention_small.cu has the errors); over the bf16
-// cache P is rounded to bf16.  The maximum that exponents refer to moves only when it has grown by 2^8, so O is
+// eight take 103; moving the bits by integer operations instead of the cvt, 141.)  K's place frees when S is done,
+// V's when O is.  Q's rows are scaled by a power of two into fp16's range there, and P is rounded to fp16
+// (attention_small.cu has the errors); over the bf16 cache P is rounded to bf16.  The maximum that exponents refer to moves only when it has grown by 2^8, so O is
 // rarely rescaled; sums, maxima and O are in fp32.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -32,10 +38,6 @@
 #include "attn_share.cuh"
 #include "common.cuh"
 
-#ifndef FMAB
-#define FMAB 0
-#define FMAQ 0
-#endif
 namespace nld {
 
 namespace {
@@ -52,14 +54,12 @@ template <typename E>
 struct Wide {   // bf16
   static constexpr bool kQ8 = false;
   static constexpr int kK = 6, kV = 6, kRaw = 0;        // tiles of K, of V, raw ones
-  static constexpr int kFma = FMAB;                        // of 16 exponentials, those on the multiply-add pipe
   static constexpr int kThreads = kSoftmax + 96;        // two issuing warps, a loading one
 };
 template <>
 struct Wide<__nv_fp8_storage_t> {
   static constexpr bool kQ8 = true;
   static constexpr int kK = 4, kV = 4, kRaw = 4;
-  static constexpr int kFma = FMAQ;
   static constexpr int kThreads = kSoftmax + 96 + 256;   // and eight converting ones
 };
 template <typename E>
@@ -129,26 +129,6 @@ NLD_DEV f2 fma2(f2 a, f2 b, f2 c) {
   f2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
-}
-NLD_DEV f2 both(float a) { return pair(a, a); }
-// 2^x of two numbers on the multiply-add pipe, relative error 2^-23: x = n + f, |f| <= 1/2, by adding 1.5 2^23; 2^f
-// by its Chebyshev interpolant of degree 5; n into the exponent.  x under -126 counts as -126, x <= 126.
-NLD_DEV void exp2_fma(f2 x, float& y0, float& y1) {
-  float a, b;
-  unpair(x, a, b);
-  x = pair(fmaxf(a, -126.f), fmaxf(b, -126.f));
-  const f2 t = add2(x, both(12582912.f));
-  const f2 f = fma2(add2(t, both(-12582912.f)), both(-1.f), x);
-  f2 p = fma2(f, both(0.001339086336f), both(0.009676031918f));
-  p = fma2(f, p, both(0.05550357114f));
-  p = fma2(f, p, both(0.2402210749f));
-  p = fma2(f, p, both(0.693147188f));
-  p = fma2(f, p, both(1.f));
-  float t0, t1;
-  unpair(t, t0, t1);
-  unpair(p, a, b);
-  y0 = __uint_as_float(__float_as_uint(a) + (__float_as_uint(t0) << 23));
-  y1 = __uint_as_float(__float_as_uint(b) + (__float_as_uint(t1) << 23));
 }
 template <bool kHalf>
 NLD_DEV uint32_t pack16(float lo, float hi) {
@@ -276,6 +256,49 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
+  int n_issued = 0;   // tiles requested (load_thr)
+  const int* table = a.page_table + static_cast<size_t>(b) * a.pps;
+  // tile j's K and V (e4m3: both raw) into their stages; false: a wait ran out
+  auto request = [&](int j) -> bool {
+    const int page = table[t_lo + j];
+    const bool bad = page < 0 || page >= a.n_pages;
+    if (bad) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
+    if constexpr (kQ8) {
+      const int st = j % W::kRaw;
+      if (j >= W::kRaw && !mbar_wait(&raw_empty[st], static_cast<uint32_t>(j / W::kRaw - 1) & 1u, kWait)) return false;
+      ++n_issued;
+      s_bad[st] = bad;
+      mbar_arrive_expect_tx(&raw_full[st], 2 * kRawBytes);
+      const uint8_t* kp = static_cast<const uint8_t*>(a.pool) + (static_cast<size_t>(bad ? 0 : page) * 2 * a.Hkv + g) * kRawBytes;
+      bulk_load(sRaw + (st * 2) * kRawBytes, kp, kRawBytes, &raw_full[st]);
+      bulk_load(sRaw + (st * 2 + 1) * kRawBytes, kp + static_cast<size_t>(a.Hkv) * kRawBytes, kRawBytes, &raw_full[st]);
+    } else {
+      const int st = j % W::kK;
+      if (j >= W::kK && !mbar_wait(&k_empty[st], static_cast<uint32_t>(j / W::kK - 1) & 1u, kWait)) return false;
+      // (a page outside the pool: rows outside the tensor, which read as zeros)
+      mbar_arrive_expect_tx(&k_full[st], kTileBytes);
+#pragma unroll
+      for (int box = 0; box < 2; ++box)
+        tma_load_2d(sK + st * kTileBytes + box * kBoxBytes, &tmKV, &k_full[st], box * 64, bad ? -kPage : (page * 2 * a.Hkv + g) * kPage);
+      if (j >= W::kV && !mbar_wait(&v_empty[st], static_cast<uint32_t>(j / W::kV - 1) & 1u, kWait)) {
+        mbar_wait(&k_full[st], static_cast<uint32_t>(j / W::kK) & 1u, kWait);   // the copies in flight land
+        return false;
+      }
+      ++n_issued;
+      mbar_arrive_expect_tx(&v_full[st], kTileBytes);
+#pragma unroll
+      for (int box = 0; box < 2; ++box)
+        tma_load_2d(sV + st * kTileBytes + box * kBoxBytes, &tmKV, &v_full[st], box * 64,
+                    bad ? -kPage : ((page * 2 + 1) * a.Hkv + g) * kPage);
+    }
+    return true;
+  };
+  // e4m3: the first tiles come while Q is laid out (97 -> 95 us; over bf16 pages, without a conversion behind them, the
+  // block of 32 with a shared prefix took 104 us that way and 98 without)
+  constexpr int kAhead = kQ8 ? W::kRaw : 0;
+  if (load_thr)
+    for (int j = 0; j < min(kAhead, ntile); ++j) request(j);
+
   // Q into tensor memory, two dims a column: thread (stream x, row r) writes dims 64 x .. of row r
   const int x = tid >> 7, r = tid & 127;   // softmax threads
   float c = a.scale_log2;                  // the scores' scale to log2 units
@@ -326,51 +349,9 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
 
   bool aborted = false;
   float m_ref = -INFINITY, l_sum = 0.f;
-  int n_issued = 0;   // tiles requested (load_thr)
-  const int* table = a.page_table + static_cast<size_t>(b) * a.pps;
   if (load_thr) {
     // ---------------------------------------------------------------- loads --
-    for (int j = 0; j < ntile; ++j) {
-      const int page = table[t_lo + j];
-      const bool bad = page < 0 || page >= a.n_pages;
-      if (bad) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
-      if constexpr (kQ8) {
-        const int st = j % W::kRaw;
-        if (j >= W::kRaw && (!mbar_wait(&raw_empty[st], static_cast<uint32_t>(j / W::kRaw - 1) & 1u, kWait))) {
-          aborted = true;
-          break;
-        }
-        ++n_issued;
-        s_bad[st] = bad;
-        mbar_arrive_expect_tx(&raw_full[st], 2 * kRawBytes);
-        const uint8_t* kp = static_cast<const uint8_t*>(a.pool) + (static_cast<size_t>(bad ? 0 : page) * 2 * a.Hkv + g) * kRawBytes;
-        bulk_load(sRaw + (st * 2) * kRawBytes, kp, kRawBytes, &raw_full[st]);
-        bulk_load(sRaw + (st * 2 + 1) * kRawBytes, kp + static_cast<size_t>(a.Hkv) * kRawBytes, kRawBytes, &raw_full[st]);
-      } else {
-        const int st = j % W::kK;
-        if (j >= W::kK && (!mbar_wait(&k_empty[st], static_cast<uint32_t>(j / W::kK - 1) & 1u, kWait))) {
-          aborted = true;
-          break;
-        }
-        // (a page outside the pool: rows outside the tensor, which read as zeros)
-        mbar_arrive_expect_tx(&k_full[st], kTileBytes);
-#pragma unroll
-        for (int box = 0; box < 2; ++box)
-          tma_load_2d(sK + st * kTileBytes + box * kBoxBytes, &tmKV, &k_full[st], box * 64,
-                      bad ? -kPage : (page * 2 * a.Hkv + g) * kPage);
-        if (j >= W::kV && (!mbar_wait(&v_empty[st], static_cast<uint32_t>(j / W::kV - 1) & 1u, kWait))) {
-          mbar_wait(&k_full[st], static_cast<uint32_t>(j / W::kK) & 1u, kWait);   // the copies in flight land
-          aborted = true;
-          break;
-        }
-        ++n_issued;
-        mbar_arrive_expect_tx(&v_full[st], kTileBytes);
-#pragma unroll
-        for (int box = 0; box < 2; ++box)
-          tma_load_2d(sV + st * kTileBytes + box * kBoxBytes, &tmKV, &v_full[st], box * 64,
-                      bad ? -kPage : ((page * 2 + 1) * a.Hkv + g) * kPage);
-      }
-    }
+    for (int j = kAhead; j < ntile && !aborted; ++j) aborted = !request(j);
     if (aborted) {
       *s_abort = 1;
       set_err(a.err, NLD_DEVERR_TIMEOUT);
@@ -507,13 +488,9 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
         for (int k = 0; k < 16; ++k) {
           const f2 e2 = fma2(pair(__uint_as_float(s[h][2 * k]), __uint_as_float(s[h][2 * k + 1])), c2, nb2);
           float p0, p1;
-          if (k % 16 >= 16 - W::kFma) {
-            exp2_fma(e2, p0, p1);
-          } else {
-            unpair(e2, p0, p1);
-            p0 = exp2_hw(p0);
-            p1 = exp2_hw(p1);
-          }
+          unpair(e2, p0, p1);
+          p0 = exp2_hw(p0);
+          p1 = exp2_hw(p1);
           ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
           p[h][k] = pack16<kQ8>(p0, p1);
         }
@@ -634,18 +611,22 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     }
     const bool take = __any_sync(0xffffffffu, w1 != 0.f);   // (a stream without a tile has no O)
 #pragma unroll 2
-    for (int u = 0; u < 8; ++u) {
-      float o[16];
+    for (int u = 0; u < 4; ++u) {
+      uint32_t o[32];
       if (take) {
-        tmem_ld16(o_at + u * 16, o);
+        tmem_ld32_nowait(o_at + u * 32, o);
+        tmem_wait_ld(o);
       } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = 0.f;
+        for (int k = 0; k < 32; ++k) o[k] = 0u;
       }
 #pragma unroll
-      for (int k = 0; k < 16; k += 4) {
-        float4* at = reinterpret_cast<float4*>(sO + r * 128 + ((((u * 16 + k) >> 2) ^ (r & 31)) << 2));
-        float4 v = w1 != 0.f ? make_float4(o[k] * w1, o[k + 1] * w1, o[k + 2] * w1, o[k + 3] * w1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < 32; k += 4) {
+        float4* at = reinterpret_cast<float4*>(sO + r * 128 + (((u * 8 + (k >> 2)) ^ (r & 31)) << 2));
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w1 != 0.f)
+          v = make_float4(__uint_as_float(o[k]) * w1, __uint_as_float(o[k + 1]) * w1, __uint_as_float(o[k + 2]) * w1,
+                          __uint_as_float(o[k + 3]) * w1);
         if (add && w0 != 0.f) {
           const float4 z = *at;
           v = make_float4(fmaf(z.x, w0, v.x), fmaf(z.y, w0, v.y), fmaf(z.z, w0, v.z), fmaf(z.w, w0, v.w));

@@ -2250,8 +2250,15 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
   return NLD_OK;
 }
 
-// Rows of a kv head (positions x heads) up to which the kernel for small query tiles serves a call.
-constexpr int kSmallRowsQ8 = 32, kSmallRowsShared = 64;
+// The kernel for small query tiles (mma.sync: its time grows with the rows of a kv head, positions x heads) or the one for
+// wide ones (tcgen05: a page costs the same for 1 row or 128, a launch 4 us more)?  Measured, small against wide,
+// 32 query and 8 kv heads: e4m3, 32 rows, 64 sequences of 2000 keys 101 / 125 us, 8 of 16000 117 / 102, 48 rows 68 / 36;
+// a shared prefix, 16 rows 15.3 / 17.0 us at 4000 keys and 35.3 / 34.5 at 16000, 32 rows 16.7 / 16.8 at 2000 and 56.8 /
+// 34.8 at 16000, 64 rows 98 / 36.
+static bool small_tiles(long long rows, bool prefix, int keys) {
+  if (prefix && keys > 2048) return rows <= 16;
+  return rows <= 32;
+}
 
 // Argument checks common to the attention operators below.
 static nld_status attn_check(const void* d_q, const void* d_kv_pool, const int32_t* d_page_table, int pages_per_seq,
@@ -2302,7 +2309,7 @@ nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float*
     a.err = d_err;
   };
   cudaError_t e;
-  if (static_cast<long long>(m) * G <= kSmallRowsQ8) {
+  if (small_tiles(static_cast<long long>(m) * G, false, max_len)) {
     AttnSmallArgs a{};
     fill(a);
     attn_small_plan(batch, max_len, sms, a);
@@ -2353,7 +2360,7 @@ nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const in
   // profiling hook serves both passes.
   auto pass = [&](int share, int seqs, int rows, const int32_t* table, int pps, int max_keys, bool pdl, bool launch) -> nld_status {
     cudaError_t e = cudaSuccess;
-    if (g_attn_kernel.load() == 0 && static_cast<long long>(rows) * G <= kSmallRowsShared) {
+    if (g_attn_kernel.load() == 0 && small_tiles(static_cast<long long>(rows) * G, share == kPrefixPass, max_keys)) {
       AttnSmallArgs a{};
       a.q = d_q;
       a.out = d_out;
