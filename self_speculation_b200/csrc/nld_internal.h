@@ -245,7 +245,8 @@ struct SampleArgs {
   const float* min_p;
   int* tokens;
   float* prob;                  // [rows] or null
-  int S, part;                  // CTAs of a row, 16-byte vectors of a warp's part of a slice (set by the launcher)
+  int S, part, head;            // CTAs of a row, 16-byte vectors of a warp's part of a slice, bytes before the slice in
+                                // shared memory (set by the launcher)
 };
 
 // ---- host-side launchers (each returns cudaError_t of the launch) -----------------------

@@ -15,8 +15,16 @@
 // halving of the weight; the next over the order-preserving keys inside the border's bin, until
 // that bin is one key (three levels for fp32, two for bf16, whatever the values).  Every
 // CTA counts its slice; one cluster barrier later each of them finds the bin from all CTAs'
-// range sums and that range's bins over distributed shared memory.  Where the first histogram leaves
-// at most kList tokens (most calls with top-k, and peaked rows), one CTA ranks them against one
+// range sums and that range's bins over distributed shared memory.
+//
+// Adding to shared memory is what a histogram costs (18 cycles a warp), so the first levels add less:
+//   - for a small k, of each thread's largest logit alone: the k-th of those bounds the border from below, and
+//     the tokens from there on are few;
+//   - for p, one 32-bit number a token, its weight over that of its bin's start, to 2^-15: two or three bins that
+//     must hold the border.  The next pass takes the exact total and the exact mass over those bins in
+//     registers and counts the tokens inside exactly.  If the border is not there after all, the exact first
+//     level follows.
+// Where at most kList tokens are left (most calls with top-k, and peaked rows), one CTA ranks them against one
 // another instead, and neither further levels nor another pass over the row follow.
 //
 // Masses are sums of 64-bit fixed-point weights (2^44 at the row's largest logit; up to 2^19
@@ -32,13 +40,12 @@ namespace nld {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 16;       // of a CTA: 16, or 8 (see the launcher)
 constexpr int kMaxS = 8;            // CTAs of a row
 constexpr int kBins = 1024;
 constexpr int kRanges = 32;         // of 32 bins
 constexpr float kPerOctave = 20.f;  // bins per halving: the last one starts at 2^-51, no weight
-constexpr int kList = kThreads / 2;   // tokens ranked against one another
+constexpr int kList = 256;          // tokens ranked against one another
 constexpr float kFltMax = 3.402823466e38f;
 constexpr double kOne = 17592186044416.0;   // 2^44: the weight of the largest logit
 
@@ -121,11 +128,12 @@ struct Weigh {
     tab = tab_;
   }
   // Bin of the first level of a logit not under `low`: not falling as x falls.
-  NLD_DEV int bin(float x) const {
+  NLD_DEV float depth(float x) const {   // in bins
     float d = (half_top - 0.5f * fminf(x, kFltMax)) * steps;
     if (more != 1.f) d *= more;
-    return static_cast<int>(fminf(d, static_cast<float>(kBins - 1)));
+    return fminf(d, static_cast<float>(kBins - 1));
   }
+  NLD_DEV int bin(float x) const { return static_cast<int>(depth(x)); }
   // exp((x - top) / T) 2^44 + 2^52, rounded to a whole number, as the bits of the double (kBias + the
   // weight); kBias where !in, or where x is under `low` and not in.  With y = 16 log2(e) (x - top) / T = k + r,
   // |r| <= 1/2: 2^(y / 16) = 2^(k / 16) p(r), p the Chebyshev interpolant of degree 5 of 2^(r / 16) with p(0)
@@ -184,7 +192,7 @@ NLD_DEV V warp_scan(V v) {
   }
   return v;
 }
-// Sum over the threads before this one, and over all.  `red` holds kWarps entries; callable again at
+// Sum over the threads before this one, and over all.  `red` holds an entry a warp; callable again at
 // once.
 template <typename V>
 __device__ __noinline__ V block_scan(V v, V* red, V& total) {
@@ -193,7 +201,7 @@ __device__ __noinline__ V block_scan(V v, V* red, V& total) {
   __syncthreads();
   if (lane == 31) red[warp] = inc;
   __syncthreads();
-  const V w = lane < kWarps ? red[lane] : V(0);
+  const V w = lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : V(0);
   const V before = warp_sum(lane < warp ? w : V(0));
   total = warp_sum(w);
   return before + inc - v;
@@ -219,31 +227,39 @@ NLD_DEV void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); 
 
 // What a CTA's peers read, and its own scratch.
 struct Shared {
-  union {
-    uint32_t hist[2][3][kBins];        // [buffer][limb][bin]; counts use limb 0
-    struct {
-      u64 all[kList], weight[kList];   // rank 0, after the searches: the lists of all CTAs, the tokens' weights
-    };
-  };
-  u64 range[2][kRanges];        // [buffer]: sums over 32 bins
-  u64 list[kList];              // key, then the index's complement
-  u64 part_mass[kWarps];        // kept mass over the border, ties at it: of each warp's part of the slice
-  int part_ties[kWarps];
+  u64 part_mass[kMaxWarps];     // kept mass over the border, ties at it: of each warp's part of the slice
+  int part_ties[kMaxWarps];
   double tab[16];
   Weigh weigh;
-  u64 red_m[kWarps];
-  int red_c[kWarps];
+  u64 red_m[kMaxWarps], red_n[kMaxWarps];
+  int red_c[kMaxWarps];
   uint32_t top;                 // the slice's largest key
   int top_at;                   // the lowest index of the row's largest logit in the slice
   int listed;                   // tokens of `list` (more: not all are in it)
   int found_at;                 // warp 0's findings
   uint32_t key_lo, key_hi;
   u64 found_before, found_with, found_total;
+  int found_count;
+  u64 sum_total, sum_above;     // of the slice: mass, and that over the bins that must hold the border
+  int sum_count;                // tokens in and over those bins
   int at_part, done;            // the sampled token's part, and what lies before that part
   u64 at_before, total;
   long long at_ties;
   double target;
+  // from here on only where there is a border to find
+  u64 range[2][kRanges];        // [buffer]: sums over 32 bins
+  u64 gather[3][kMaxS][32];     // of the CTAs of the row: their range sums, their sums of one range's bins
+  u64 sums[kMaxS][3];           // their sum_total, sum_above, sum_count
+  u64 list[kList];              // key, then the index's complement
+  union {
+    uint32_t hist[2][3][kBins];        // [buffer][limb][bin]; counts use limb 0
+    struct {
+      u64 all[kList], weight[kList];   // rank 0, after the searches: the lists of all CTAs, the tokens' weights
+    };
+  };
 };
+constexpr size_t kHeadFull = (sizeof(Shared) + 15) / 16 * 16;
+constexpr size_t kHeadPlain = (offsetof(Shared, range) + 15) / 16 * 16;
 
 // One row's slice: the 16-byte vectors of it, in shared memory or (slices over the shared memory)
 // straight from global memory; -inf outside the row.
@@ -287,18 +303,19 @@ struct Slice {
   }
 };
 
-template <typename T, bool kStaged>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+template <typename T, bool kStaged, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 1024 / (32 * kWarps)) sample_kernel(const SampleArgs a) {
+  constexpr int kThreads = 32 * kWarps;
   using K = Key<T>;
   constexpr int n = K::n;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
-  constexpr size_t kHead = (sizeof(Shared) + 15) / 16 * 16;
+  uint4* const stage = reinterpret_cast<uint4*>(smem + a.head);
   const int S = a.S, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % S;
   const size_t row = blockIdx.x / S;
   Slice<T, kStaged> slice;
-  slice.staged = reinterpret_cast<const uint4*>(smem + kHead);
+  slice.staged = stage;
   slice.row = static_cast<const T*>(a.logits) + row * a.ld;
   slice.vocab = a.vocab;
   // the row's vectors start at the 16-byte boundary at or before it; warp w of the slice has a.part of them
@@ -338,11 +355,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (by_k || by_p) clear(0);
 
   // the largest logit
+  float big = -INFINITY;   // of this thread's
   {
-    float big = -INFINITY;
     const int w0 = max(v0, slice.whole0), w1 = min(v1, slice.whole1);
     if constexpr (kStaged) {   // all of the slice in flight; a thread reads back what it copied itself
-      uint4* const to = reinterpret_cast<uint4*>(smem + kHead);
+      uint4* const to = stage;
       for (int v = w0 + lane; v < w1; v += 32) cp_async16(to + v, slice.vector(v));
       cp_async_wait();
       for (int v = w0 + lane; v < w1; v += 32) big = fmaxf(big, K::most(to[v]));
@@ -354,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       for (int v = v0 + lane; v < v1; v += 32)
         if (!slice.whole(v)) {
           const uint4 got = slice.ragged(v);
-          if constexpr (kStaged) reinterpret_cast<uint4*>(smem + kHead)[v] = got;
+          if constexpr (kStaged) stage[v] = got;
           big = fmaxf(big, K::most(got));
         }
     const uint32_t key = __reduce_max_sync(0xffffffffu, K::of(big));
@@ -405,18 +422,75 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   auto over_border = [&]() {   // logits from here on are over the border and have a weight
     return border >= top_key ? NAN : fmaxf(weigh.low, K::value(border + 1));   // (NaN: none are)
   };
-  bool mass = !by_k;       // what is searched for: by number first, then by mass among the kept
+  // What is searched for, by number first, then by mass among the kept: kMaxima, kCount or kBracketing, kBracketed,
+  // kMass are first levels of it
+  enum { kMaxima, kCount, kBracketing, kBracketed, kMass };
+  int kind = !by_k ? kBracketing : k <= kList - 16 ? kMaxima : kCount;
   int level = 0, buf = 0;
   u64 before = 0, rest = 0, rest_w = 0;   // over the bin; mass of the ties at the top-k border, and of one of them
-  double limit = by_k ? k : p;            // level 0 by mass: a share of the total
-  uint32_t lo = 0, hi = 0;                // keys of the bin (levels 1 and up)
+  double limit = by_k ? k : p;            // first levels by mass: a share of the total
+  uint32_t lo = 0, hi = 0;                // keys of the bin (levels 1 and up, and kBracketed)
+  u64 above = 0;                          // kBracketed: mass of this thread's tokens over above_x
+  float above_x = INFINITY;
   while (by_k || by_p) {
     // One level: tokens over the border (level 0) or with keys lo..hi, in steps of 2^shift; their numbers or masses
     // by bin, and the bin with which the sum reaches the limit.
+    const bool mass = kind >= kBracketing, by_key = level > 0 || kind == kBracketed;
     uint32_t(*h)[kBins] = sh.hist[buf];
-    const int shift = level > 0 ? max(0, 22 - __clz(hi - lo)) : 0;   // (hi - lo) >> shift < 2^10
-    {
-      const float from = level == 0 ? over_border() : K::value(lo), to = level == 0 ? INFINITY : K::value(hi);
+    const int shift = by_key ? max(0, 22 - __clz(hi - lo)) : 0;   // (hi - lo) >> shift < 2^10
+    const float from = level == 0 ? over_border() : K::value(lo), to = by_key ? K::value(hi) : INFINITY;
+    auto add = [&](int bin, u64 w) {
+      uint32_t* const at = &h[0][0] + bin;
+      const uint32_t w2 = static_cast<uint32_t>(w >> 30), w1 = static_cast<uint32_t>(w >> 15) & 0x7fffu;
+      atomicAdd(at, static_cast<uint32_t>(w) & 0x7fffu);
+      if (w1) atomicAdd(at + kBins, w1);
+      if (w2) atomicAdd(at + 2 * kBins, w2);
+    };
+    if (level == 0 && kind == kMaxima) {
+      if (big >= from) atomicAdd(&h[0][weigh.bin(big)], 1u);
+    } else if (level == 0 && kind == kBracketing) {
+      for (int q = q0 + lane; q < q1; q += 32) {
+        float x[4];
+        slice.get(q, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (x[e] >= from) {
+            const float d = weigh.depth(x[e]);
+            const int b = static_cast<int>(d);
+            atomicAdd(&h[0][b], __float2uint_rn(32768.f * exp2f((static_cast<float>(b) - d) * (1.f / kPerOctave))));
+          }
+      }
+    } else if (level == 0 && kind == kBracketed) {
+      const float from_lo = K::value(lo);
+      u64 all = 0;
+      int count = 0;
+      above = 0;
+      above_x = to;
+      for (int q = q0 + lane; q < q1; q += 32) {
+        float x[4];
+        slice.get(q, x);
+        if (!(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)) continue;
+        u64 w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = weigh.biased(x[e], x[e] >= from) - Weigh::kBias;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          all += w[e];
+          if (x[e] > to) above += w[e];
+          if (x[e] >= from_lo) {
+            ++count;
+            if (x[e] <= to) add(static_cast<int>((hi - K::of(x[e])) >> shift), w[e]);
+          }
+        }
+      }
+      const u64 s0 = warp_sum(all), s1 = warp_sum(above);
+      const int s2 = __reduce_add_sync(0xffffffffu, count);
+      if (lane == 0) {
+        sh.red_m[warp] = s0;
+        sh.red_n[warp] = s1;
+        sh.red_c[warp] = s2;
+      }
+    } else {
       for (int q = q0 + lane; q < q1; q += 32) {
         float x[4];
         slice.get(q, x);
@@ -424,116 +498,196 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 #pragma unroll
         for (int e = 0; e < 4; ++e) in[e] = x[e] >= from && x[e] <= to;
         if (!(in[0] || in[1] || in[2] || in[3])) continue;
-        u64 w[4];
-        int bin[4];
-        if (mass) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = weigh.biased(x[e], in[e]) - Weigh::kBias;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) bin[e] = level == 0 ? weigh.bin(x[e]) : static_cast<int>((hi - K::of(x[e])) >> shift);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (!in[e]) continue;
-          uint32_t* const at = &h[0][0] + bin[e];
-          if (mass) {
-            const uint32_t w2 = static_cast<uint32_t>(w[e] >> 30), w1 = static_cast<uint32_t>(w[e] >> 15) & 0x7fffu;
-            atomicAdd(at, static_cast<uint32_t>(w[e]) & 0x7fffu);
-            if (w1) atomicAdd(at + kBins, w1);
-            if (w2) atomicAdd(at + 2 * kBins, w2);
-          } else {
-            atomicAdd(at, 1u);
-          }
+          const int bin = by_key ? static_cast<int>((hi - K::of(x[e])) >> shift) : weigh.bin(x[e]);
+          if (mass) add(bin, fixed_weight(sh.weigh, x[e]));
+          else atomicAdd(&h[0][bin], 1u);
         }
       }
     }
     __syncthreads();
+    const bool bracketing = level == 0 && kind == kBracketing;
+    // a bin's sum (counts: the other limbs are 0; bracketing: of the weights over 2^15, as a double)
+    auto bin_sum = [&](uint32_t w0, uint32_t w1, uint32_t w2, int b) -> u64 {
+      if (bracketing) return static_cast<u64>(__double_as_longlong(static_cast<double>(w0) * exp2f(-b * (1.f / kPerOctave))));
+      return w0 + (static_cast<u64>(w1) << 15) + (static_cast<u64>(w2) << 30);
+    };
+    auto plus = [&](u64 a_, u64 b_) -> u64 {
+      if (bracketing) return static_cast<u64>(__double_as_longlong(__longlong_as_double(a_) + __longlong_as_double(b_)));
+      return a_ + b_;
+    };
 #pragma unroll 1
     for (int r = warp; r < kRanges; r += kWarps) {
-      const int b = r * 32 + lane;   // (counts: the other limbs are 0)
-      const u64 s = warp_sum(h[0][b] + (static_cast<u64>(h[1][b]) << 15) + (static_cast<u64>(h[2][b]) << 30));
+      const int b = r * 32 + lane;
+      u64 s = bin_sum(h[0][b], h[1][b], h[2][b], b);
+#pragma unroll 1
+      for (int off = 16; off > 0; off >>= 1) s = plus(s, __shfl_xor_sync(0xffffffffu, s, off));
       if (lane == 0) sh.range[buf][r] = s;
+    }
+    if (warp == 0 && level == 0 && kind == kBracketed) {
+      const u64 s0 = warp_sum(lane < kWarps ? sh.red_m[lane] : 0), s1 = warp_sum(lane < kWarps ? sh.red_n[lane] : 0);
+      const int s2 = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.red_c[lane] : 0);
+      if (lane == 0) {
+        sh.sum_total = s0;
+        sh.sum_above = s1;
+        sh.sum_count = s2;
+      }
     }
     row_sync();
     // the other buffer was last read before this barrier
     clear(buf ^ 1);
-    if (warp == 0) {
-      u64 s = 0;
-#pragma unroll
-      for (int q = 0; q < kMaxS; ++q)
-        if (q < S) s += peer64(&sh.range[buf][lane], q);
-      u64 inc = warp_scan(s);
-      const u64 total = __shfl_sync(0xffffffffu, inc, 31) + rest;
-      double reach = limit;
-      if (mass && level == 0) reach *= static_cast<double>(total);
-      auto reached = [&](u64 c) { return static_cast<double>(before + c) >= reach; };
-      uint32_t m = __ballot_sync(0xffffffffu, reached(inc));
-      int found = -1;
-      u64 with = 0, ahead = before;
-      if (m) {
-        const int r = __ffs(m) - 1;
-        const u64 base = __shfl_sync(0xffffffffu, inc - s, r);
-        const int b = r * 32 + lane;
-        u64 t = 0;
-#pragma unroll
-        for (int q = 0; q < kMaxS; ++q)
-          if (q < S)
-            t += peer32(&h[0][b], q) + (static_cast<u64>(peer32(&h[1][b], q)) << 15) + (static_cast<u64>(peer32(&h[2][b], q)) << 30);
-        inc = warp_scan(t);
-        m = __ballot_sync(0xffffffffu, reached(base + inc));
-        const int l = __ffs(m) - 1;
-        with = before + base + __shfl_sync(0xffffffffu, inc, l);
-        ahead += base + __shfl_sync(0xffffffffu, inc - t, l);
-        found = r * 32 + l;
-      }
-      uint32_t klo = 0, khi = 0;
-      if (found >= 0 && level == 0) {
-        // lowest keys of bins <= found and of bins < found, by 32 probes at a time: keys (none, most], `most` is one
-        khi = top_key;
+    // The row's sums, in two steps: warp q fetches CTA q's range sums, then its bins of the range with the border (a
+    // warp that fetched all of them waited 4 us: a fetch is 0.2 us and the next one came after its use).
+    auto scan = [&](u64 v) -> u64 {   // over the lanes up to and with this one
 #pragma unroll 1
-        for (int b = found; b >= max(0, found - 1); --b) {
-          uint32_t none = max(border, K::of(weigh.low) - 1), most = top_key;   // (keys under weigh.low: no weight)
+      for (int off = 1; off < 32; off <<= 1) {
+        const u64 o = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v = plus(v, o);
+      }
+      return v;
+    };
+    auto of_all = [&](const u64(*g)[32]) -> u64 {
+      u64 v = g[0][lane];
+#pragma unroll 1
+      for (int q = 1; q < S; ++q) v = plus(v, g[q][lane]);
+      return v;
+    };
+    if (warp < S) {
+      sh.gather[0][warp][lane] = peer64(&sh.range[buf][lane], warp);
+      if (level == 0 && kind == kBracketed && lane < 3)
+        sh.sums[warp][lane] = lane == 0 ? peer64(&sh.sum_total, warp) : lane == 1 ? peer64(&sh.sum_above, warp) : peer32(&sh.sum_count, warp);
+    }
+    __syncthreads();
+    const int sides = bracketing ? 2 : 1;
+    if (warp < max(S, 2)) {
+      const u64 inc = scan(of_all(sh.gather[0]));
+      u64 total = __shfl_sync(0xffffffffu, inc, 31);
+      u64 start = before;   // what lies before the bins
+      int count = 0;
+      double reach = limit;
+      if (level == 0 && kind == kBracketed) {
+        total = start = 0;
+#pragma unroll 1
+        for (int q = 0; q < S; ++q) {
+          total += sh.sums[q][0];
+          start += sh.sums[q][1];
+          count += static_cast<int>(sh.sums[q][2]);
+        }
+      }
+      total += bracketing ? 0 : rest;
+      if (level == 0 && mass && !bracketing) reach *= static_cast<double>(total);
+      if (bracketing) reach *= __longlong_as_double(total) + static_cast<double>(rest) * (32768.0 / kOne);
+      // the bin with which the sum reaches the limit; bracketing: the first that may be it (side 0), and the first that is
+      // surely at it or behind (a bin's sum is off by 2^-14 of it at most)
+      auto reached = [&](u64 c, int side) {
+        if (bracketing) return __longlong_as_double(c) * (side == 0 ? 1.0 + 0x1p-13 : 1.0 - 0x1p-13) >= reach;
+        return static_cast<double>(start + c) >= reach;
+      };
+      int r[2];
+#pragma unroll
+      for (int side = 0; side < 2; ++side) r[side] = __ffs(__ballot_sync(0xffffffffu, reached(inc, side))) - 1;
+      if (warp < S)
+#pragma unroll 1
+        for (int side = 0; side < sides; ++side)
+          if (r[side] >= 0) {
+            const int b = r[side] * 32 + lane;
+            const uint32_t w0 = peer32(&h[0][b], warp), w1 = bracketing ? 0 : peer32(&h[1][b], warp), w2 = bracketing ? 0 : peer32(&h[2][b], warp);
+            sh.gather[1 + side][warp][lane] = bin_sum(w0, w1, w2, b);
+          }
+      if (S == 1) __syncwarp();
+      named_bar_sync(1, 32 * max(S, 2));
+      // warp 0 finds the bin and its lowest key, warp 1 the highest one; bracketing: warp 0 the first bin's highest
+      // key, warp 1 the last one's lowest
+      if (warp < 2) {
+        const int side = bracketing ? warp : 0, range = r[side];
+        int found = -1;
+        u64 with = 0, ahead = start;
+        if (range >= 0) {
+          const u64 base = __shfl_sync(0xffffffffu, inc, range > 0 ? range - 1 : 0);
+          const u64 t = of_all(sh.gather[1 + side]), sub = scan(t);
+          const uint32_t m = __ballot_sync(0xffffffffu, reached(range > 0 ? plus(base, sub) : sub, side));
+          const int l = m ? __ffs(m) - 1 : 31;   // (sums of doubles in another order: the last, then)
+          if (!bracketing) {
+            with = start + (range > 0 ? base : 0) + __shfl_sync(0xffffffffu, sub, l);
+            ahead = with - __shfl_sync(0xffffffffu, t, l);
+          }
+          found = range * 32 + l;
+        }
+        const uint32_t under = max(border, K::of(weigh.low) - 1);   // keys from here down: kept by nothing, or no weight
+        // lowest key of a bin <= b: the keys about where fp32 has it, else by 32 probes at a time; (none, most], `most` is one
+        auto lowest = [&](int b) -> uint32_t {
+          uint32_t none = under, most = top_key;
+          bool near = true;
           while (most - none > 1) {
             const uint32_t step = (most - none + 31) / 32;
-            const u64 probe64 = static_cast<u64>(none) + static_cast<u64>(step) * (lane + 1);
+            u64 probe64 = static_cast<u64>(none) + static_cast<u64>(step) * (lane + 1);
+            if (near) {
+              const uint32_t g = K::of(weigh.top - 2.f * static_cast<float>(b + 1) / (weigh.steps * weigh.more));
+              probe64 = static_cast<u64>(max(g, none + 16)) - 15 + lane;
+              near = false;
+            }
             const uint32_t probe = probe64 < most ? static_cast<uint32_t>(probe64) : most;
-            const int first = __ffs(__ballot_sync(0xffffffffu, weigh.bin(K::value(probe)) <= b)) - 1;
-            most = __shfl_sync(0xffffffffu, probe, first);
-            if (first > 0) none = __shfl_sync(0xffffffffu, probe, first - 1);
+            const uint32_t is = __ballot_sync(0xffffffffu, weigh.bin(K::value(probe)) <= b);
+            const int first = is ? __ffs(is) - 1 : 32;
+            const uint32_t lower = __shfl_sync(0xffffffffu, probe, first > 0 ? first - 1 : 0);
+            if (first < 32) most = __shfl_sync(0xffffffffu, probe, first & 31);
+            if (first > 0) none = lower;
           }
-          if (b == found) klo = most;
-          else khi = most - 1;
+          return most;
+        };
+        if (by_key) {
+          if (warp == 0 && lane == 0) {
+            const uint32_t khi = hi - (static_cast<uint32_t>(found) << shift);
+            sh.key_hi = khi;
+            sh.key_lo = khi - lo < (1u << shift) ? lo : khi - ((1u << shift) - 1);
+          }
+        } else if (warp == (bracketing ? 0 : 1)) {
+          const uint32_t khi = found > 0 ? lowest(found - 1) - 1 : top_key;
+          if (lane == 0) sh.key_hi = khi;
+        } else {
+          const uint32_t klo = found >= 0 ? lowest(found) : under + 1;   // (bracketing: not surely reached)
+          if (lane == 0) sh.key_lo = klo;
         }
-      } else if (found >= 0) {
-        khi = hi - (static_cast<uint32_t>(found) << shift);
-        klo = khi - lo < (1u << shift) ? lo : khi - ((1u << shift) - 1);
-      }
-      if (lane == 0) {
-        sh.found_at = found;
-        sh.found_before = ahead;
-        sh.found_with = with;
-        sh.found_total = total;
-        sh.key_lo = klo;
-        sh.key_hi = khi;
+        if (warp == 0 && lane == 0) {
+          bool missed = bracketing && found < 0;   // not there after all
+          if (level == 0 && kind == kBracketed) missed = static_cast<double>(start) >= reach || (found < 0 && lo > under + 1);
+          sh.found_at = missed ? -2 : found;
+          sh.found_before = ahead;
+          sh.found_with = with;
+          sh.found_total = total;
+          sh.found_count = count;
+        }
       }
     }
     __syncthreads();
     buf ^= 1;
+    if (bracketing || sh.found_at == -2) {
+      if (sh.found_at == -2) above_x = INFINITY;
+      kind = sh.found_at == -2 ? kMass : kBracketed;
+      lo = sh.key_lo;
+      hi = sh.key_hi;
+      continue;
+    }
     const bool found = sh.found_at >= 0;
-    if (mass && level == 0) limit *= static_cast<double>(sh.found_total);
+    if (mass && level == 0) {
+      limit *= static_cast<double>(sh.found_total);
+      if (!found) above_x = INFINITY;
+    }
     before = found ? sh.found_before : sh.found_total - rest;
     lo = sh.key_lo;
     hi = sh.key_hi;
-    if (found && level == 0 && (mass || sh.found_with <= kList)) {
+    if (found && level == 0 && (kind == kMaxima || kind == kMass || (kind == kCount ? sh.found_with : sh.found_count) <= kList)) {
       // the tokens down to the bin's last key into the lists
-      const float from = K::value(lo);
+      const float from_lo = K::value(lo);
       for (int q = q0 + lane; q < q1 && *static_cast<volatile int*>(&sh.listed) <= kList; q += 32) {
         float x[4];
         slice.get(q, x);
-        if (!(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)) continue;
+        if (!(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from_lo)) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (x[e] >= from) {
+          if (x[e] >= from_lo) {
             const int at = atomicAdd(&sh.listed, 1);
             if (at < kList)
               sh.list[at] = (static_cast<u64>(K::of(x[e])) << 32) |
@@ -554,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
         if (S > 1) cluster_arrive();   // the lists are read
         if (rank == 0) {
-          // 2 to 16 lanes an entry, each against its share of the others
+          // 1 to 16 lanes an entry, each against its share of the others
           int lanes = 16;
           while (lanes * count > kThreads) lanes >>= 1;
           const int at = tid / lanes, sub = tid % lanes;
@@ -601,6 +755,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         if (S > 1) cluster_wait();
         return;
       }
+      if (kind == kMaxima) {   // too many: the lists start over
+        row_sync();
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+      }
+    }
+    if (kind == kMaxima) {
+      kind = kCount;
+      before = 0;
+      continue;
     }
     ++level;
     if (found && lo != hi) continue;
@@ -609,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     if (!mass) {
       if (found) ties = k - static_cast<long long>(before);
       if (!by_p) break;
-      mass = true;
+      kind = kBracketing;
       level = 0;
       limit = p;
       before = 0;
@@ -637,10 +801,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   const float cut = over_border();
   const bool filtered = border != K::kInf || least > 0 || !weigh.plain();
   u64 border_w = 0;
-  if (border != K::kInf && border_x >= weigh.low) {
-    border_w = fixed_weight(sh.weigh, border_x);
-    border_w = border_w >= least ? border_w : 0;
-  }
+  if (border != K::kInf && border_x >= weigh.low) border_w = fixed_weight(sh.weigh, border_x);
+  // the mass over the bracket is known already, if min-p takes nothing of it
+  const bool known = above_x != INFINITY && border_w >= least;
+  if (border_w < least) border_w = 0;
   // mass over the border and ties of each warp's part of the slice
   {
     u64 s = 0;
@@ -659,14 +823,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         float x[4];
         slice.get(q, x);
         for (int e = 0; e < 4; ++e) c += x[e] == border_x;
-        if (!(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= cut)) continue;
+        bool in[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) in[e] = x[e] >= cut && (!known || x[e] <= above_x);
+        if (!(in[0] || in[1] || in[2] || in[3])) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const u64 w = weigh.biased(x[e], x[e] >= cut) - Weigh::kBias;
+          const u64 w = weigh.biased(x[e], in[e]) - Weigh::kBias;
           s += w >= least ? w : 0;
         }
       }
     }
+    if (known) s += above;
     s = warp_sum(s);
     c = warp_sum(c);
     if (lane == 0) {
@@ -676,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   }
   row_sync();
   if (warp == 0) {   // the part with the token: a lane has up to 4 of the parts in a row
-    const int per = S >= 2 ? S / 2 : 1;
+    const int per = max(1, S * kWarps / 32);
     u64 m[4];
     int t[4], t_sum = 0;
 #pragma unroll
@@ -781,31 +949,41 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 template <typename T>
 cudaError_t launch(cudaStream_t st, SampleArgs a, int sms) {
   constexpr int n = Key<T>::n;
-  constexpr size_t kHead = (sizeof(Shared) + 15) / 16 * 16;
+  constexpr size_t kMost = 200 * 1024;
   const long long vectors = (static_cast<long long>(a.vocab) + 2 * (n - 1)) / n;   // with a row's skew
+  a.head = static_cast<int>(a.top_k || a.top_p ? kHeadFull : kHeadPlain);
   // CTAs per row: so that two of them, slices and all, fit an SM's shared memory; more while the machine
-  // has room for them and each keeps 4096 logits
-  int S = 1;
+  // has room for them and each keeps 4096 logits.  Many rows without a border to find: 8-warp CTAs of up to 52 KB, four
+  // an SM, so that one loads while others weigh (300 bf16 rows of 151936: FILLME).
+  int S = 1, warps = 16;
   while (S < kMaxS && vectors * 16 > S * 80 * 1024LL) S *= 2;
   while (S < kMaxS && 2LL * S * a.rows <= 2LL * sms && a.vocab >= 2 * S * 4096) S *= 2;
+  if (!a.top_k && !a.top_p && vectors * 16 <= kMaxS * 52 * 1024LL && 1LL * S * a.rows > 2LL * sms) {
+    warps = 8;
+    while (S < kMaxS && vectors * 16 > S * 52 * 1024LL) S *= 2;
+  }
   a.S = S;
-  a.part = static_cast<int>((vectors + S * kWarps - 1) / (S * kWarps));
-  const size_t bytes = kHead + static_cast<size_t>(a.part) * kWarps * 16;
-  const bool staged = bytes <= 200 * 1024;
-  auto* kernel = staged ? sample_kernel<T, true> : sample_kernel<T, false>;
+  a.part = static_cast<int>((vectors + S * warps - 1) / (S * warps));
+  const size_t bytes = a.head + static_cast<size_t>(a.part) * warps * 16;
+  const bool staged = bytes <= kMost;
+  if (!staged) {   // (slices of 2^16 logits at most, as the histogram's counters need)
+    warps = 16;
+    a.part = static_cast<int>((vectors + S * warps - 1) / (S * warps));
+  }
+  auto* kernel = !staged ? sample_kernel<T, false, 16> : warps == 16 ? sample_kernel<T, true, 16> : sample_kernel<T, true, 8>;
   cudaError_t e;
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  static std::atomic<bool> ready[64];   // per device: the staged kernel's shared-memory limit
+  static std::atomic<bool> ready[64];   // per device: the staged kernels' shared-memory limit
   if (staged && (dev >= 64 || !ready[dev].load(std::memory_order_acquire))) {
-    if ((e = cudaFuncSetAttribute(sample_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024)) != cudaSuccess)
-      return e;
+    for (auto* k : {sample_kernel<T, true, 16>, sample_kernel<T, true, 8>})
+      if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost)) != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * S);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = staged ? bytes : kHead;
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = staged ? bytes : a.head;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
