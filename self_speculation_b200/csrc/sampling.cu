@@ -11,7 +11,7 @@
 //
 // The kept tokens are those whose logit exceeds a border value and the first few, by index, that
 // equal it.  A border is found by histograms of counts (top-k) or masses (top-p), of kBins bins
-// in the order of falling logits: the first over equal steps of (max x - x) / T, kPerOctave per
+// in the order of falling logits: the first over equal steps of (max x - x) / T, kOctave per
 // halving of the weight; the next over the order-preserving keys inside the border's bin, until
 // that bin is one key (three levels for fp32, two for bf16, whatever the values).  Every
 // CTA counts its slice; one cluster barrier later each of them finds the bin from all CTAs'
@@ -44,7 +44,7 @@ constexpr int kMaxWarps = 16;       // of a CTA: 16, or 8 (see the launcher)
 constexpr int kMaxS = 8;            // CTAs of a row
 constexpr int kBins = 1024;
 constexpr int kRanges = 32;         // of 32 bins
-constexpr float kPerOctave = 20.f;  // bins per halving: the last one starts at 2^-51, no weight
+constexpr int kOctave = 20;         // bins per halving: the last one starts at 2^-51, no weight
 constexpr int kList = 256;          // tokens ranked against one another
 constexpr float kFltMax = 3.402823466e38f;
 constexpr double kOne = 17592186044416.0;   // 2^44: the weight of the largest logit
@@ -122,7 +122,7 @@ struct Weigh {
     s16 = inv_t * 23.083120654223414;   // 16 log2(e)
     // 50 halvings down (fp32 rounding leaves it under 120); 2^-45 rounds to nothing
     low = top_ > kFltMax ? top_ : fmaxf(static_cast<float>(top_d - 34.657 * static_cast<double>(temperature)), -kFltMax);
-    const double per = inv_t * (2.0 * 1.4426950408889634 * kPerOctave);
+    const double per = inv_t * (2.0 * 1.4426950408889634 * kOctave);
     steps = static_cast<float>(fmin(per, 1e38));
     more = per > 1e38 ? static_cast<float>(per * 1e-38) : 1.f;
     tab = tab_;
@@ -174,6 +174,12 @@ __device__ __noinline__ double real_weight(const Weigh& w, float x) {   // not r
   double p;
   const double scaled = w.parts(fminf(fmaxf(x, w.low), kFltMax), true, p);
   return scaled * p;
+}
+
+NLD_DEV float exp2_hw(float x) {   // relative error about 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <typename V>
@@ -457,7 +463,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1024 / (32 * kWarps)) sample_kern
           if (x[e] >= from) {
             const float d = weigh.depth(x[e]);
             const int b = static_cast<int>(d);
-            atomicAdd(&h[0][b], __float2uint_rn(32768.f * exp2f((static_cast<float>(b) - d) * (1.f / kPerOctave))));
+            atomicAdd(&h[0][b], __float2uint_rn(exp2_hw(fmaf(static_cast<float>(b) - d, 1.f / kOctave, 15.f))));
           }
       }
     } else if (level == 0 && kind == kBracketed) {
@@ -509,21 +515,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1024 / (32 * kWarps)) sample_kern
     }
     __syncthreads();
     const bool bracketing = level == 0 && kind == kBracketing;
-    // a bin's sum (counts: the other limbs are 0; bracketing: of the weights over 2^15, as a double)
+    // a bin's sum (counts: the other limbs are 0; bracketing: of the weights to 2^-15, 2^43 for the largest logit's)
     auto bin_sum = [&](uint32_t w0, uint32_t w1, uint32_t w2, int b) -> u64 {
-      if (bracketing) return static_cast<u64>(__double_as_longlong(static_cast<double>(w0) * exp2f(-b * (1.f / kPerOctave))));
+      if (bracketing) {
+        const int o = b / kOctave;
+        return (static_cast<u64>(w0) * __float2uint_rn(exp2f(28.f - static_cast<float>(b - o * kOctave) * (1.f / kOctave)))) >> o;
+      }
       return w0 + (static_cast<u64>(w1) << 15) + (static_cast<u64>(w2) << 30);
-    };
-    auto plus = [&](u64 a_, u64 b_) -> u64 {
-      if (bracketing) return static_cast<u64>(__double_as_longlong(__longlong_as_double(a_) + __longlong_as_double(b_)));
-      return a_ + b_;
     };
 #pragma unroll 1
     for (int r = warp; r < kRanges; r += kWarps) {
       const int b = r * 32 + lane;
-      u64 s = bin_sum(h[0][b], h[1][b], h[2][b], b);
-#pragma unroll 1
-      for (int off = 16; off > 0; off >>= 1) s = plus(s, __shfl_xor_sync(0xffffffffu, s, off));
+      const u64 s = warp_sum(bin_sum(h[0][b], h[1][b], h[2][b], b));
       if (lane == 0) sh.range[buf][r] = s;
     }
     if (warp == 0 && level == 0 && kind == kBracketed) {
@@ -540,19 +543,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1024 / (32 * kWarps)) sample_kern
     clear(buf ^ 1);
     // The row's sums, in two steps: warp q fetches CTA q's range sums, then its bins of the range with the border (a
     // warp that fetched all of them waited 4 us: a fetch is 0.2 us and the next one came after its use).
-    auto scan = [&](u64 v) -> u64 {   // over the lanes up to and with this one
-#pragma unroll 1
-      for (int off = 1; off < 32; off <<= 1) {
-        const u64 o = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v = plus(v, o);
-      }
-      return v;
-    };
     auto of_all = [&](const u64(*g)[32]) -> u64 {
-      u64 v = g[0][lane];
-#pragma unroll 1
-      for (int q = 1; q < S; ++q) v = plus(v, g[q][lane]);
-      return v;
+      u64 v[kMaxS], sum = 0;
+#pragma unroll
+      for (int q = 0; q < kMaxS; ++q) v[q] = g[min(q, S - 1)][lane];   // (all fetched before the first is used)
+#pragma unroll
+      for (int q = 0; q < kMaxS; ++q) sum += q < S ? v[q] : 0;
+      return sum;
     };
     if (warp < S) {
       sh.gather[0][warp][lane] = peer64(&sh.range[buf][lane], warp);
@@ -562,7 +559,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1024 / (32 * kWarps)) sample_kern
     __syncthreads();
     const int sides = bracketing ? 2 : 1;
     if (warp < max(S, 2)) {
-      const u64 inc = scan(of_all(sh.gather[0]));
+      const u64 inc = warp_scan(of_all(sh.gather[0]));
       u64 total = __shfl_sync(0xffffffffu, inc, 31);
       u64 start = before;   // what lies before the bins
       int count = 0;
@@ -578,12 +575,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1024 / (32 * kWarps)) sample_kern
       }
       total += bracketing ? 0 : rest;
       if (level == 0 && mass && !bracketing) reach *= static_cast<double>(total);
-      if (bracketing) reach *= __longlong_as_double(total) + static_cast<double>(rest) * (32768.0 / kOne);
+      if (bracketing) reach *= static_cast<double>(total) + 0.5 * static_cast<double>(rest);
       // the bin with which the sum reaches the limit; bracketing: the first that may be it (side 0), and the first that is
       // surely at it or behind (a bin's sum is off by 2^-14 of it at most)
       auto reached = [&](u64 c, int side) {
-        if (bracketing) return __longlong_as_double(c) * (side == 0 ? 1.0 + 0x1p-13 : 1.0 - 0x1p-13) >= reach;
-        return static_cast<double>(start + c) >= reach;
+        const double d = static_cast<double>(start + c);
+        return (bracketing ? d * (side == 0 ? 1.0 + 0x1p-13 : 1.0 - 0x1p-13) : d) >= reach;
       };
       int r[2];
 #pragma unroll
@@ -606,9 +603,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1024 / (32 * kWarps)) sample_kern
         u64 with = 0, ahead = start;
         if (range >= 0) {
           const u64 base = __shfl_sync(0xffffffffu, inc, range > 0 ? range - 1 : 0);
-          const u64 t = of_all(sh.gather[1 + side]), sub = scan(t);
-          const uint32_t m = __ballot_sync(0xffffffffu, reached(range > 0 ? plus(base, sub) : sub, side));
-          const int l = m ? __ffs(m) - 1 : 31;   // (sums of doubles in another order: the last, then)
+          const u64 t = of_all(sh.gather[1 + side]), sub = warp_scan(t);
+          const int l = __ffs(__ballot_sync(0xffffffffu, reached((range > 0 ? base : 0) + sub, side))) - 1;
           if (!bracketing) {
             with = start + (range > 0 ? base : 0) + __shfl_sync(0xffffffffu, sub, l);
             ahead = with - __shfl_sync(0xffffffffu, t, l);
@@ -954,7 +950,7 @@ cudaError_t launch(cudaStream_t st, SampleArgs a, int sms) {
   a.head = static_cast<int>(a.top_k || a.top_p ? kHeadFull : kHeadPlain);
   // CTAs per row: so that two of them, slices and all, fit an SM's shared memory; more while the machine
   // has room for them and each keeps 4096 logits.  Many rows without a border to find: 8-warp CTAs of up to 52 KB, four
-  // an SM, so that one loads while others weigh (300 bf16 rows of 151936: FILLME).
+  // an SM, so that one loads while others weigh (300 bf16 rows of 151936: 86 -> 80 us).
   int S = 1, warps = 16;
   while (S < kMaxS && vectors * 16 > S * 80 * 1024LL) S *= 2;
   while (S < kMaxS && 2LL * S * a.rows <= 2LL * sms && a.vocab >= 2 * S * 4096) S *= 2;
