@@ -14,9 +14,11 @@
 // another (lens -> page table, lens -> angles).  Squares, norm and rotation are in fp32, two numbers
 // an instruction; the only roundings are those to the output types.
 //
-// 3 blocks an SM (72 registers) and 4 heads a thread measured best: ragged prefill of 8 x 2048 rows of
-// 40 + 2 x 8 heads into an e4m3 cache 64 us, 2 blocks 75, 2 heads a thread 79 (4 blocks); chunks
-// staged through shared memory by cp.async, a persistent warp per token, 87.
+// 24 warps an SM (80 registers) and 4 heads a thread measured best: ragged prefill of 8 x 2048 rows of
+// 40 + 2 x 8 heads into an e4m3 cache (186 MB) 62 us, 16 warps 75, 28 or 32 warps with spills 68 to 70; 2 heads a thread
+// 79; chunks staged through shared memory by cp.async, a persistent warp per token, 87; gains folded into the
+// rotation's coefficients, warps of q heads or of k and v heads alone, 66.  The same loads and stores without the
+// arithmetic take 40 us: what bounds it is arithmetic and loads that overlap in part.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -85,7 +87,7 @@ NLD_DEV void store_vec(__nv_fp8_storage_t* p, const float* x) {
     *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 
-constexpr int kQkvThreads = 256;
+constexpr int kQkvThreads = 128;
 constexpr int kU = 4;   // heads of a thread
 
 // Two fp32 numbers worked on by one instruction.
@@ -122,7 +124,7 @@ NLD_DEV float divide(float x, float sc, float r) {
 }
 
 template <typename T, typename C, int kHd>
-__global__ void __launch_bounds__(kQkvThreads, 3) qkv_write_kernel(const QkvWriteArgs a) {
+__global__ void __launch_bounds__(kQkvThreads, 6) qkv_write_kernel(const QkvWriteArgs a) {
   constexpr int n = Vec<T>::n;
   constexpr int half = kHd / 2;
   constexpr int lanes = half / n;         // threads per head: 4, 8 or 16
