@@ -694,12 +694,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1024 / (32 * kWarps)) sample_kern
       const int count = __reduce_add_sync(0xffffffffu, lane < S ? static_cast<int>(peer32(&sh.listed, lane)) : 0);
       if (count <= kList) {   // (the same in every CTA)
         if (rank == 0) {
-          int first = 0;   // every thread an entry of one of the lists
-          for (int q = 0; q < S; ++q) {
-            const int c = static_cast<int>(peer32(&sh.listed, q));
-            if (tid >= first && tid < first + c) sh.all[tid] = peer64(&sh.list[tid - first], q);
-            first += c;
+          // every thread an entry of one of the lists
+          const int c = lane < S ? static_cast<int>(peer32(&sh.listed, lane)) : 0;
+          const int end = warp_scan(c);
+          int q = 0, first = 0;
+          for (int i = 0; i < S - 1; ++i) {
+            const int e = __shfl_sync(0xffffffffu, end, i);
+            if (tid >= e) {
+              q = i + 1;
+              first = e;
+            }
           }
+          if (tid < count) sh.all[tid] = peer64(&sh.list[tid - first], q);
           __syncthreads();
         }
         if (S > 1) cluster_arrive();   // the lists are read
@@ -717,11 +723,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1024 / (32 * kWarps)) sample_kern
           int rank_of = 0;
           u64 over = 0;
           if (in)
-            for (int j = sub; j < count; j += lanes)
-              if (sh.all[j] > mine) {
-                ++rank_of;
-                over += sh.weight[j];
-              }
+#pragma unroll 4
+            for (int j = sub; j < count; j += lanes) {
+              const bool ahead = sh.all[j] > mine;
+              const u64 o = sh.weight[j];
+              rank_of += ahead;
+              over += ahead ? o : 0;
+            }
           for (int off = 1; off < lanes; off <<= 1) {
             rank_of += __shfl_xor_sync(0xffffffffu, rank_of, off);
             over += __shfl_xor_sync(0xffffffffu, over, off);
@@ -739,8 +747,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1024 / (32 * kWarps)) sample_kern
           const uint32_t code = static_cast<uint32_t>(mine);   // falls as the index rises
           u64 sum = 0;
           if (in)
-            for (int j = sub; j < count; j += lanes)
-              if (static_cast<uint32_t>(sh.all[j]) > code) sum += sh.weight[j];
+#pragma unroll 4
+            for (int j = sub; j < count; j += lanes) {
+              const u64 o = sh.weight[j];
+              sum += static_cast<uint32_t>(sh.all[j]) > code ? o : 0;
+            }
           for (int off = 1; off < lanes; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
           const double target = u * static_cast<double>(total);
           if (keep && sub == 0 && static_cast<double>(sum) <= target && static_cast<double>(sum + w) > target) {
@@ -844,13 +855,22 @@ __global__ void __launch_bounds__(32 * kWarps, 1024 / (32 * kWarps)) sample_kern
     u64 m[4];
     int t[4], t_sum = 0;
 #pragma unroll
+    for (int j = 0; j < 4; ++j) {   // (every fetch of another CTA's before the first use)
+      const int part = min(lane * per + j, S * kWarps - 1);
+      const u64* const pm = &sh.part_mass[part % kWarps];
+      const int* const pt = &sh.part_ties[part % kWarps];
+      m[j] = S == 1 ? *pm : 0;
+      t[j] = S == 1 ? *pt : 0;
+      if (S > 1) {
+        m[j] = ld_dsmem_u64(dsmem_addr(smem_u32(pm), part / kWarps));
+        t[j] = static_cast<int>(ld_dsmem_u32(dsmem_addr(smem_u32(pt), part / kWarps)));
+      }
+    }
+#pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int part = lane * per + j;
-      m[j] = 0;
-      t[j] = 0;
-      if (j < per && part < S * kWarps) {
-        m[j] = peer64(&sh.part_mass[part % kWarps], part / kWarps);
-        t[j] = static_cast<int>(peer32(&sh.part_ties[part % kWarps], part / kWarps));
+      if (j >= per || lane * per + j >= S * kWarps) {
+        m[j] = 0;
+        t[j] = 0;
       }
       t_sum += t[j];
     }
