@@ -488,7 +488,8 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
  *                anything (NaN patterns too).
  *   d_k_scale, d_v_scale  [Hkv] fp32.
  *   d_err        one int32 or NULL: a lens[b] outside 0..pages_per_seq*64-m is clamped, a page id
- *                outside the pool reads as zeros, and NLD_DEVERR_KV_OVERFLOW is or-ed in.
+ *                outside the pool reads as zeros, and NLD_DEVERR_KV_OVERFLOW is or-ed in;
+ *                NLD_DEVERR_TIMEOUT if a bounded wait ran out.
  * The other arguments, the mask and the conventions are those of nld_attention (d_q and d_out
  * bf16, 16-byte aligned).  Scores, maxima and sums are fp32; the probabilities are rounded to fp16 for
  * their product with V.
@@ -509,10 +510,12 @@ nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float*
  *                   position_offset of nld_qk_norm_rope).
  *   d_workspace     16-byte aligned, nld_attention_shared_workspace_size() bytes: the prefix's fp32
  *                   partial of every (row, query head).  Calls sharing it must not overlap.
- *   d_err           one int32 or NULL: a lens[b] outside 0..pages_per_seq*64-m is clamped and
- *                   NLD_DEVERR_KV_OVERFLOW is or-ed in; NLD_DEVERR_TIMEOUT if a bounded wait ran out.
- * Slots behind a sequence's last key, and behind the prefix's, may hold anything.
- * Two launches on `cuda_stream`; returns after them.
+ *   d_err           one int32 or NULL: a lens[b] outside 0..pages_per_seq*64-m is clamped, a page id
+ *                   outside the pool reads as zeros, and NLD_DEVERR_KV_OVERFLOW is or-ed in;
+ *                   NLD_DEVERR_TIMEOUT if a bounded wait ran out.
+ * Slots behind a sequence's last key, and behind the prefix's, may hold anything.  Scores, maxima and sums
+ * are fp32; the probabilities are rounded to bf16 for their product with V.
+ * Two launches on `cuda_stream` (one with shared_len 0); returns after them.
  */
 size_t nld_attention_shared_workspace_size(int batch, int m, int n_q_heads);
 nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const int32_t* d_shared_pages,

@@ -20,9 +20,6 @@
 // each leaves its unnormalised partial (O, running max, running sum) in its shared memory, and
 // after a cluster barrier every CTA merges a slice of the rows by reading all partials over
 // distributed shared memory, in split order.  No global scratch, no atomics.
-#include <atomic>
-
-#include "attn_share.cuh"
 #include "common.cuh"
 
 namespace nld {
@@ -130,14 +127,7 @@ NLD_DEV void tmem_ld_wait_regs(uint32_t (&r)[16]) {
 // so only the bf16 K/V cache rounds; the output is written as (hi, lo) bf16 row pairs, the
 // operand layout of the O projection.  Otherwise (the stand-alone entry point) q and the output
 // are plain bf16 and P is rounded to bf16 for its MMA.
-//
-// kShare (the shared-prefix attention, nld_attention_shared): kOwnPass and kPrefixPass are its two
-// launches.  The prefix pass takes the rows of every sequence as the rows of one (batch 1, m =
-// batch x m), lets all of them see the key_end keys of the prefix's pages, and leaves each row's
-// merged partial (O unnormalised, max, sum) in global memory in fp32.  The own pass is the plain
-// attention over a sequence's own pages whose final merge takes that partial in as one more split.
-// Both zero the V rows behind the last key, so that pages may hold anything there.
-template <bool kHiLo, int kMaxW, int kShare>
+template <bool kHiLo, int kMaxW>
 __global__ void __launch_bounds__(32 * kMaxW, 1)
     attn_mma_kernel(const __grid_constant__ CUtensorMap tmKV, const AttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -180,10 +170,10 @@ __global__ void __launch_bounds__(32 * kMaxW, 1)
   // earlier forwards (kernels that completed before the one this launch may overlap: that one
   // writes only rows len..len+m-1), so the first KV tiles lying wholly in the cached prefix are
   // requested before waiting for the previous kernel.
-  int len = kShare == kPrefixPass ? a.key_end : a.lens[b];
+  int len = a.lens[b];
   const int p0 = qt * a.QT;
   const int np = min(a.QT, a.m - p0);
-  if (kShare != kPrefixPass && (len < 0 || len + a.m > a.pps * kPage)) {   // keys must stay inside the page table row
+  if (len < 0 || len + a.m > a.pps * kPage) {   // keys must stay inside the page table row
     if (tid == 0) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
     len = max(0, min(len, a.pps * kPage - a.m));
   }
@@ -193,7 +183,7 @@ __global__ void __launch_bounds__(32 * kMaxW, 1)
     // the CTA's last row sees the furthest key (both intervals grow with the row)
     int v1, l2, h2;
     row_keys(len, p0 + np - 1, a.block_size, a.m, crow, a.quad_k, v1, l2, h2);
-    kv_end = kShare == kPrefixPass ? len : max(v1, h2) + 1;
+    kv_end = max(v1, h2) + 1;
   }
   const int n_tiles = (kv_end + kPage - 1) / kPage;
   // at least min_tiles KV tiles per split: fewer, fuller splits keep the merge short
@@ -228,7 +218,7 @@ __global__ void __launch_bounds__(32 * kMaxW, 1)
       if (u < n_pre) issue_page(u, pg[u]);
   }
   __syncwarp();
-  if constexpr (kShare != kOwnPass) pdl_wait();   // (the own pass waits for the prefix partials, at its merge)
+  pdl_wait();
   stamp(1);
   if (tid == 0) {
 #pragma unroll
@@ -301,7 +291,6 @@ __global__ void __launch_bounds__(32 * kMaxW, 1)
     row_keys(len, p0 + ra / a.G, a.block_size, a.m, crow, a.quad_k, vis_a, la2, ha2);
   if (rb < a.rows && rb / a.G < np)
     row_keys(len, p0 + rb / a.G, a.block_size, a.m, crow, a.quad_k, vis_b, lb2, hb2);
-  if constexpr (kShare == kPrefixPass) vis_a = vis_b = len - 1;   // (padding rows too: never stored)
 
   float o[16][4];
 #pragma unroll
@@ -325,13 +314,6 @@ __global__ void __launch_bounds__(32 * kMaxW, 1)
     const int j0 = (t_lo + i) * kPage;
     const uint32_t kb = smem_u32(sK + stage * kKVTile);
     const uint32_t vb = smem_u32(sV + stage * kKVTile);
-    if constexpr (kShare != 0) {   // V rows behind the last key: P is 0 there, V may be anything
-      if (j0 + kPage > kv_end) {
-        for (int e = tid; e < (j0 + kPage - kv_end) * 16; e += nthr)
-          *reinterpret_cast<uint4*>(sV + stage * kKVTile + kv_off(kv_end - j0 + (e >> 4), e & 15)) = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-      }
-    }
 
     float sc[8][4];
 #pragma unroll
@@ -477,7 +459,7 @@ __global__ void __launch_bounds__(32 * kMaxW, 1)
     }
   };
 
-  if (kShare == 0 && a.S == 1) {
+  if (a.S == 1) {
     const float ia = (l_a > 0.f) ? 1.f / l_a : 0.f, ib = (l_b > 0.f) ? 1.f / l_b : 0.f;
     if (vis_a >= 0) {
 #pragma unroll
@@ -519,7 +501,6 @@ __global__ void __launch_bounds__(32 * kMaxW, 1)
   // a warp merges one row: lane q < S reads split q's (m, l) of it and the warp shares them (the
   // cluster's shared-memory reads, which bound the merge, drop by a third)
   const uint32_t ml_lane = ((tid & 31) < S) ? dsmem_addr(ml_base, tid & 31) : 0u;
-  if constexpr (kShare == kOwnPass) pdl_wait();   // the prefix pass has written its partials
   for (int e = tid; e < (r1 - r0) * 32; e += nthr) {   // warp-uniform: nthr is whole warps
     const int r = r0 + (e >> 5), d4 = e & 31;
     const int p = r / a.G;
@@ -550,10 +531,6 @@ __global__ void __launch_bounds__(32 * kMaxW, 1)
         acc.z += w * ov[q].z;
         acc.w += w * ov[q].w;
       }
-    }
-    if constexpr (kShare != 0) {
-      const size_t prow = (static_cast<size_t>(b) * a.m + p0 + p) * a.Hq + static_cast<size_t>(g * a.G + (r - p * a.G));
-      if (share_merge<kShare>(a.part_o, a.part_ml, prow, d4, M, L, acc)) continue;
     }
     const float inv = (L > 0.f) ? 1.f / L : 0.f;
     store2(r, d4 * 4, acc.x * inv, acc.y * inv);
@@ -635,7 +612,7 @@ NLD_DEV uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return d;
 }
 
-template <bool kHiLo, int kRT, int kTile, int kShare>
+template <bool kHiLo, int kRT, int kTile>
 __global__ void __launch_bounds__(tc_threads(kRT), 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmKV, const AttnArgs a) {
   static_assert(kRT == 2 || kRT == 4, "2 or 4 softmax threads per row");
@@ -722,10 +699,10 @@ __global__ void __launch_bounds__(tc_threads(kRT), 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  int len = kShare == kPrefixPass ? a.key_end : a.lens[b];
+  int len = a.lens[b];
   const int p0 = qt * a.QT;
   const int np = min(a.QT, a.m - p0);
-  if (kShare != kPrefixPass && (len < 0 || len + a.m > a.pps * kPage)) {
+  if (len < 0 || len + a.m > a.pps * kPage) {
     if (tid == 0) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
     len = max(0, min(len, a.pps * kPage - a.m));
   }
@@ -734,7 +711,7 @@ __global__ void __launch_bounds__(tc_threads(kRT), 1)
   {
     int v1, l2, h2;
     row_keys(len, p0 + np - 1, a.block_size, a.m, crow, a.quad_k, v1, l2, h2);
-    kv_end = kShare == kPrefixPass ? len : max(v1, h2) + 1;
+    kv_end = max(v1, h2) + 1;
   }
   // tiles of kTile keys (pages kPg t ..); the split plan's min_tiles counts pages
   const int n_pages = (kv_end + kPage - 1) / kPage;
@@ -781,7 +758,7 @@ __global__ void __launch_bounds__(tc_threads(kRT), 1)
   int n_pre = 0;
   if (tma_thr)
     for (; n_pre < min(NS, ntile) && (t_lo + n_pre + 1) * kTile <= len; ++n_pre) issue(n_pre);
-  if constexpr (kShare != kOwnPass) pdl_wait();   // (the own pass waits for the prefix partials, at its merge)
+  pdl_wait();
   stamp(1);
   if (tma_thr)
     for (int i = n_pre; i < min(NS, ntile); ++i) issue(i);
@@ -925,7 +902,6 @@ __global__ void __launch_bounds__(tc_threads(kRT), 1)
     // ------------------------------------- softmax: row r, keys kKT kq .. kKT kq + kKT - 1 --
     int v1 = -1, l2 = 0x7fffffff, h2 = -1;
     if (row_ok) row_keys(len, p0 + prow, a.block_size, a.m, crow, a.quad_k, v1, l2, h2);
-    if constexpr (kShare == kPrefixPass) v1 = len - 1;   // (padding rows too: never stored)
     const int lq = warp & 3;   // TMEM lane quarter
     const uint32_t lane_base = static_cast<uint32_t>(lq * 32) << 16;
     const uint32_t o_col = kOCol + kq * kOC;   // this thread's columns of O
@@ -1036,21 +1012,6 @@ __global__ void __launch_bounds__(tc_threads(kRT), 1)
         if constexpr (kHiLo) tmem_st8(tmem + lane_base + p_col + p_lo + u * 8, pl[u]);
       }
       tmem_st_wait();
-      if constexpr (kShare != 0) {
-        // V rows behind the last key: P is 0 there, V may be anything.  The tile has landed (S was
-        // computed from it), the wait makes it visible to this thread; O += P V reads it after p_full.
-        const int dead = (t_lo + j + 1) * kTile - kv_end;
-        if (dead > 0) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&full[j % NS], static_cast<uint32_t>(j / NS) & 1u, kWait))) {
-            aborted = true;
-            break;
-          }
-          uint8_t* v = sV + (j % NS) * kStage + (kTile - dead) * 128;
-          for (int e = tid; e < dead * 16; e += kTcSoftmax)
-            *reinterpret_cast<uint4*>(v + (e & 1) * kBox + (e >> 1) * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async();
-        }
-      }
       tc_fence_before();
       __syncwarp();
       if ((tid & 31) == 0) mbar_arrive(&p_full[sb]);
@@ -1150,7 +1111,6 @@ __global__ void __launch_bounds__(tc_threads(kRT), 1)
   // a warp merges one row: lane q < S reads split q's (m, L) of it and the warp shares them (the
   // cluster's shared-memory reads, which bound the merge, drop by a third)
   const uint32_t ml_lane = ((tid & 31) < S) ? dsmem_addr(ml_base, tid & 31) : 0u;
-  if constexpr (kShare == kOwnPass) pdl_wait();   // the prefix pass has written its partials
   for (int e = tid; e < (r1 - r0) * 32; e += kTcThreads) {   // warp-uniform
     const int rr = r0 + (e >> 5), d4 = e & 31;
     if (rr / a.G >= np) continue;
@@ -1178,11 +1138,6 @@ __global__ void __launch_bounds__(tc_threads(kRT), 1)
         acc.z += w * ov[q].z;
         acc.w += w * ov[q].w;
       }
-    }
-    if constexpr (kShare != 0) {
-      const int p = rr / a.G;
-      const size_t prow = (static_cast<size_t>(b) * a.m + p0 + p) * a.Hq + static_cast<size_t>(g * a.G + (rr - p * a.G));
-      if (share_merge<kShare>(a.part_o, a.part_ml, prow, d4, M, L, acc)) continue;
     }
     const float inv = (L > 0.f) ? 1.f / L : 0.f;
     if (e == tid) stamp(14);
@@ -1266,16 +1221,15 @@ namespace {
 using AttnKernel = void (*)(const CUtensorMap, const AttnArgs);
 // The instantiation for a launch: tcgen05 or mma.sync, its operand form and (mma.sync) its
 // launch bound (<= 8 or 9 warps).
-template <bool kHiLo, int kShare>
-AttnKernel attn_kernel_of(int NW, int tc, int tile) {
-  if (tc && tile == 64) return tc == 2 ? attn_tc_kernel<kHiLo, 2, 64, kShare> : attn_tc_kernel<kHiLo, 4, 64, kShare>;
-  if (tc) return tc == 2 ? attn_tc_kernel<kHiLo, 2, 128, kShare> : attn_tc_kernel<kHiLo, 4, 128, kShare>;
-  return NW > 8 ? attn_mma_kernel<kHiLo, 9, kShare> : attn_mma_kernel<kHiLo, 8, kShare>;
-}
-AttnKernel attn_kernel_for(bool hilo, int NW, int tc, int tile, int share = 0) {
-  if (share == kPrefixPass) return attn_kernel_of<false, kPrefixPass>(NW, tc, tile);
-  if (share == kOwnPass) return attn_kernel_of<false, kOwnPass>(NW, tc, tile);
-  return hilo ? attn_kernel_of<true, 0>(NW, tc, tile) : attn_kernel_of<false, 0>(NW, tc, tile);
+AttnKernel attn_kernel_for(bool hilo, int NW, int tc, int tile) {
+  if (tc && tile == 64) {
+    if (tc == 2) return hilo ? attn_tc_kernel<true, 2, 64> : attn_tc_kernel<false, 2, 64>;
+    return hilo ? attn_tc_kernel<true, 4, 64> : attn_tc_kernel<false, 4, 64>;
+  }
+  if (tc == 2) return hilo ? attn_tc_kernel<true, 2, 128> : attn_tc_kernel<false, 2, 128>;
+  if (tc) return hilo ? attn_tc_kernel<true, 4, 128> : attn_tc_kernel<false, 4, 128>;
+  if (NW > 8) return hilo ? attn_mma_kernel<true, 9> : attn_mma_kernel<false, 9>;
+  return hilo ? attn_mma_kernel<true, 8> : attn_mma_kernel<false, 8>;
 }
 }  // namespace
 
@@ -1296,29 +1250,6 @@ cudaError_t init_kernel_attributes() {
                                   optin - static_cast<int>(fa.sharedSizeBytes))) != cudaSuccess)
       return e;
   }
-  return cudaSuccess;
-}
-
-// The same for the two passes of the shared-prefix attention, once per device; the plain kernels' too:
-// the split planner asks for their occupancy, which without the opt-in is none.
-cudaError_t init_shared_attention_attributes() {
-  static std::atomic<bool> done[64];
-  int dev = 0, optin = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  if ((e = init_kernel_attributes()) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
-  for (int share : {kPrefixPass, kOwnPass})
-    for (int v = 0; v < 6; ++v) {
-      const AttnKernel k = attn_kernel_for(false, v == 0 ? 8 : 9, v < 2 ? 0 : 2 + 2 * (v & 1), v < 4 ? 64 : 128, share);
-      cudaFuncAttributes fa;
-      if ((e = cudaFuncGetAttributes(&fa, k)) != cudaSuccess) return e;
-      if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    optin - static_cast<int>(fa.sharedSizeBytes))) != cudaSuccess)
-        return e;
-    }
-  if (dev < 64) done[dev].store(true, std::memory_order_release);
   return cudaSuccess;
 }
 
@@ -1387,7 +1318,7 @@ cudaError_t launch_attention_mma(cudaStream_t st, const CUtensorMap* tmKV, const
   if (pdl) attrs[na++] = attr[0];
   cfg.attrs = attrs;
   cfg.numAttrs = na;
-  return cudaLaunchKernelEx(&cfg, attn_kernel_for(a.hilo != 0, a.NW, tc, a.tc_tile, a.share), *tmKV, a);
+  return cudaLaunchKernelEx(&cfg, attn_kernel_for(a.hilo != 0, a.NW, tc, a.tc_tile), *tmKV, a);
 }
 
 cudaError_t launch_attention_simt(cudaStream_t st, const AttnArgs& a, int batch, bool f32,

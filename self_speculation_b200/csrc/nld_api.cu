@@ -2356,12 +2356,9 @@ nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const in
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   CUtensorMap map;
   bool have_map = false;
-  // One pass: rows of `seqs` sequences of `rows` positions each, over max_keys keys at most.  A kernel forced by the
-  // profiling hook serves both passes.
+  // One pass: rows of `seqs` sequences of `rows` positions each, over max_keys keys at most.
   auto pass = [&](int share, int seqs, int rows, const int32_t* table, int pps, int max_keys, bool pdl, bool launch) -> nld_status {
-    cudaError_t e = cudaSuccess;
-    if (g_attn_kernel.load() == 0 && small_tiles(static_cast<long long>(rows) * G, share == kPrefixPass, max_keys)) {
-      AttnSmallArgs a{};
+    auto fill = [&](auto& a) {
       a.q = d_q;
       a.out = d_out;
       a.pool = d_kv_pool;
@@ -2380,65 +2377,23 @@ nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const in
       a.part_o = part_o;
       a.part_ml = part_ml;
       a.err = d_err;
+    };
+    cudaError_t e = cudaSuccess;
+    if (small_tiles(static_cast<long long>(rows) * G, share == kPrefixPass, max_keys)) {
+      AttnSmallArgs a{};
+      fill(a);
       attn_small_plan(seqs, max_keys, sms, a);
       if (static_cast<long long>(seqs) * a.r_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
       if (launch) e = launch_attention_small(st, a, seqs, pdl);
     } else {
+      AttnWideArgs a{};
+      fill(a);
+      if ((static_cast<long long>(rows) * G + 127) / 128 * seqs > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
       if (!have_map && !make_map_bf16(&map, d_kv_pool, 128, static_cast<uint64_t>(n_pages) * 2 * n_kv_heads * kPage, kPage))
         return fail(nullptr, NLD_ERR_CUDA, "tensor map encode failed (pool)");
       have_map = true;
-      if (g_attn_kernel.load() == 0) {
-        AttnWideArgs a{};
-        a.q = d_q;
-        a.out = d_out;
-        a.lens = d_lens;
-        a.page_table = table;
-        a.pps = pps;
-        a.n_pages = n_pages;
-        a.m = rows;
-        a.Hq = n_q_heads;
-        a.Hkv = n_kv_heads;
-        a.G = G;
-        a.block_size = block_size;
-        a.scale_log2 = scale_log2;
-        a.share = share;
-        a.key_end = shared_len;
-        a.part_o = part_o;
-        a.part_ml = part_ml;
-        a.err = d_err;
-        if ((static_cast<long long>(rows) * G + 127) / 128 * seqs > 65535)
-          return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
-        e = attn_wide_plan(seqs, max_keys, sms, a);
-        if (e == cudaSuccess && launch) e = launch_attention_wide(st, &map, a, seqs, pdl);
-      } else {
-        if ((e = init_shared_attention_attributes()) != cudaSuccess) {
-          cudaGetLastError();
-          return fail(nullptr, NLD_ERR_CUDA, "setting kernel shared-memory limits failed: %s", cudaGetErrorString(e));
-        }
-        AttnArgs a{};
-        a.q = d_q;
-        a.out = d_out;
-        a.out_ld = static_cast<size_t>(n_q_heads) * 128;
-        a.m = rows;
-        a.Hq = n_q_heads;
-        a.Hkv = n_kv_heads;
-        a.hd = 128;
-        a.lens = d_lens;
-        a.page_table = table;
-        a.pps = pps;
-        a.block_size = block_size;
-        a.scale_log2 = scale_log2;
-        a.share = share;
-        a.key_end = shared_len;
-        a.part_o = part_o;
-        a.part_ml = part_ml;
-        a.err = d_err;
-        attn_plan(seqs, rows, n_q_heads, n_kv_heads, max_keys, sms, a,
-                  [](int S, int NW, int stages, int tc) { return attn_device_capacity(false, S, NW, stages, tc); }, 0, 0,
-                  g_attn_kernel.load(), g_attn_tile.load(), false);
-        if (static_cast<long long>(seqs) * a.q_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
-        if (launch) e = launch_attention_mma(st, &map, a, seqs, pdl);
-      }
+      e = attn_wide_plan(seqs, max_keys, sms, a);
+      if (e == cudaSuccess && launch) e = launch_attention_wide(st, &map, a, seqs, pdl);
     }
     if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
     return NLD_OK;

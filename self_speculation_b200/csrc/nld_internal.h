@@ -139,9 +139,6 @@ struct alignas(64) ChainArgs {
   WarmPhase next[2];
 };
 
-// The two launches of the shared-prefix attention (AttnArgs::share; 0: the plain attention).
-constexpr int kOwnPass = 1, kPrefixPass = 2;
-
 struct AttnArgs {
   const void* q;        // [M, Hq, hd]
   void* out;            // [M, Hq, hd] rows out_ld elements apart (tensor-core path)
@@ -168,11 +165,6 @@ struct AttnArgs {
                         // causal; pre-draft row k+1+a*k+j sees the prefix, rows 0..a and its block
   unsigned long long* trace;   // optional per-CTA timestamps (profiling hook), or null
   int* err;
-  // shared-prefix attention
-  int share;            // 0, kOwnPass or kPrefixPass
-  int key_end;          // prefix pass: keys of the prefix
-  float* part_o;        // [tokens x Hq][128] unnormalised prefix O (own pass: null = no prefix)
-  float2* part_ml;      // [tokens x Hq] its running max (log2 units) and sum
 };
 
 // Head norm, rotation and cache write of the rows of a forward (nld_qk_norm_rope).
@@ -195,6 +187,9 @@ struct QkvWriteArgs {
   int* err;
 };
 
+// The two launches of the shared-prefix attention (`share` below; 0: nld_attention_q8).
+constexpr int kOwnPass = 1, kPrefixPass = 2;
+
 // Attention for small query tiles: over the e4m3 cache (nld_attention_q8), or a pass of the
 // shared-prefix attention over the bf16 cache.
 struct AttnSmallArgs {
@@ -210,8 +205,8 @@ struct AttnSmallArgs {
   float scale_log2;             // log2(e) / sqrt(hd)
   int share;                    // 0: e4m3; kOwnPass or kPrefixPass: bf16
   int key_end;                  // prefix pass: keys of the prefix
-  float* part_o;                // as in AttnArgs
-  float2* part_ml;
+  float* part_o;                // [tokens x Hq][128] unnormalised prefix O (own pass: null = no prefix)
+  float2* part_ml;              // [tokens x Hq] its running max (log2 units) and sum
   int* err;
 };
 
@@ -262,7 +257,6 @@ cudaError_t launch_attention_mma(cudaStream_t st, const CUtensorMap* tmKV, const
 cudaError_t launch_attention_simt(cudaStream_t st, const AttnArgs& a, int batch, bool f32,
                                   int max_kv, bool pdl);
 
-cudaError_t init_shared_attention_attributes();
 cudaError_t launch_qkv_write(cudaStream_t st, const QkvWriteArgs& a, int dtype, int kv_dtype);
 void attn_small_plan(int batch, int max_len, int sms, AttnSmallArgs& a);
 cudaError_t launch_attention_small(cudaStream_t st, const AttnSmallArgs& a, int batch, bool pdl);
