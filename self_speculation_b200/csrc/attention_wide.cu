@@ -53,18 +53,20 @@ constexpr uint64_t kWait = 2000000000ull;
 template <typename E>
 struct Wide {   // bf16
   static constexpr bool kQ8 = false;
-  static constexpr int kK = 6, kV = 6, kRaw = 0;        // tiles of K, of V, raw ones
+  static constexpr int kK = 6, kV = 6, kRaw = 0;        // tiles of K, of V, raw ones of V
+  static constexpr int kKBytes = kTileBytes;
   static constexpr int kThreads = kSoftmax + 96;        // two issuing warps, a loading one
 };
 template <>
 struct Wide<__nv_fp8_storage_t> {
   static constexpr bool kQ8 = true;
-  static constexpr int kK = 4, kV = 4, kRaw = 4;
-  static constexpr int kThreads = kSoftmax + 96 + 256;   // and eight converting ones
+  static constexpr int kK = 6, kV = 4, kRaw = 4;
+  static constexpr int kKBytes = kRawBytes;
+  static constexpr int kThreads = kSoftmax + 96 + 128;   // and four converting ones
 };
 template <typename E>
 __host__ __device__ constexpr int wide_bytes() {
-  return 1024 + (Wide<E>::kK + Wide<E>::kV) * kTileBytes + Wide<E>::kRaw * 2 * kRawBytes + 512;
+  return 1024 + Wide<E>::kK * Wide<E>::kKBytes + Wide<E>::kV * kTileBytes + Wide<E>::kRaw * kRawBytes + 512;
 }
 
 NLD_DEV void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -72,6 +74,15 @@ NLD_DEV void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same with e4m3 operands, 32 of K a product, four to a column of A.
+NLD_DEV void tc_mma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -154,6 +165,20 @@ NLD_DEV bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
   return p != 0;
 }
+// Four numbers as e4m3, and what that leaves of them as e4m3.
+NLD_DEV void split_e4m3(const float (&q)[4], uint32_t& hi, uint32_t& lo) {
+  hi = lo = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    uint32_t back, none;
+    halves_of(h, back, none);
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
+    hi |= h << (16 * i);
+    lo |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(q[2 * i] - b.x, q[2 * i + 1] - b.y), __NV_SATFINITE, __NV_E4M3))
+          << (16 * i);
+  }
+}
 NLD_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
@@ -174,9 +199,9 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sK = smem;                          // [kK] tiles
-  uint8_t* sV = sK + W::kK * kTileBytes;       // [kV]
-  uint8_t* sRaw = sV + W::kV * kTileBytes;     // [kRaw][K, V]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sRaw + W::kRaw * 2 * kRawBytes);
+  uint8_t* sV = sK + W::kK * W::kKBytes;       // [kV]
+  uint8_t* sRaw = sV + W::kV * kTileBytes;     // [kRaw] of V
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sRaw + W::kRaw * kRawBytes);
   uint64_t* k_full = bars;             // [kK] tile of K there
   uint64_t* k_empty = bars + 6;        // [kK] S of the tile done
   uint64_t* v_full = bars + 12;        // [kV]
@@ -203,7 +228,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < W::kK; ++i) {
-      mbar_init(&k_full[i], kQ8 ? 4 : 1);
+      mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < W::kV; ++i) {
@@ -212,7 +237,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     }
     for (int i = 0; i < W::kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 8);
+      mbar_init(&raw_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -225,7 +250,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     mbar_init(fin, 2);
     *s_abort = 0;
     fence_mbar_init();
-    if constexpr (!kQ8) tma_prefetch_desc(&tmKV);
+    tma_prefetch_desc(&tmKV);
   }
   if (warp == kSoftmax / 32) {
     tmem_alloc(s_tmem, 512);   // S and P of the streams, O of the streams, Q
@@ -263,32 +288,34 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     const int page = table[t_lo + j];
     const bool bad = page < 0 || page >= a.n_pages;
     if (bad) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
+    const int ks = j % W::kK;
+    if (j >= W::kK && !mbar_wait(&k_empty[ks], static_cast<uint32_t>(j / W::kK - 1) & 1u, kWait)) return false;
+    // (a page outside the pool: rows outside the tensor, which read as zeros)
+    const int k_row = bad ? -kPage : (page * 2 * a.Hkv + g) * kPage;
+    mbar_arrive_expect_tx(&k_full[ks], W::kKBytes);
     if constexpr (kQ8) {
-      const int st = j % W::kRaw;
-      if (j >= W::kRaw && !mbar_wait(&raw_empty[st], static_cast<uint32_t>(j / W::kRaw - 1) & 1u, kWait)) return false;
-      ++n_issued;
-      s_bad[st] = bad;
-      mbar_arrive_expect_tx(&raw_full[st], 2 * kRawBytes);
-      const uint8_t* kp = static_cast<const uint8_t*>(a.pool) + (static_cast<size_t>(bad ? 0 : page) * 2 * a.Hkv + g) * kRawBytes;
-      bulk_load(sRaw + (st * 2) * kRawBytes, kp, kRawBytes, &raw_full[st]);
-      bulk_load(sRaw + (st * 2 + 1) * kRawBytes, kp + static_cast<size_t>(a.Hkv) * kRawBytes, kRawBytes, &raw_full[st]);
+      tma_load_2d(sK + ks * W::kKBytes, &tmKV, &k_full[ks], 0, k_row);
     } else {
-      const int st = j % W::kK;
-      if (j >= W::kK && !mbar_wait(&k_empty[st], static_cast<uint32_t>(j / W::kK - 1) & 1u, kWait)) return false;
-      // (a page outside the pool: rows outside the tensor, which read as zeros)
-      mbar_arrive_expect_tx(&k_full[st], kTileBytes);
+#pragma unroll
+      for (int box = 0; box < 2; ++box) tma_load_2d(sK + ks * kTileBytes + box * kBoxBytes, &tmKV, &k_full[ks], box * 64, k_row);
+    }
+    const int vs = j % (kQ8 ? W::kRaw : W::kV), vn = j / (kQ8 ? W::kRaw : W::kV);
+    if (vn > 0 && !mbar_wait(kQ8 ? &raw_empty[vs] : &v_empty[vs], static_cast<uint32_t>(vn - 1) & 1u, kWait)) {
+      mbar_wait(&k_full[ks], static_cast<uint32_t>(j / W::kK) & 1u, kWait);   // the copies in flight land
+      return false;
+    }
+    ++n_issued;
+    if constexpr (kQ8) {
+      s_bad[vs] = bad;
+      mbar_arrive_expect_tx(&raw_full[vs], kRawBytes);
+      bulk_load(sRaw + vs * kRawBytes,
+                static_cast<const uint8_t*>(a.pool) + ((static_cast<size_t>(bad ? 0 : page) * 2 + 1) * a.Hkv + g) * kRawBytes, kRawBytes,
+                &raw_full[vs]);
+    } else {
+      mbar_arrive_expect_tx(&v_full[vs], kTileBytes);
 #pragma unroll
       for (int box = 0; box < 2; ++box)
-        tma_load_2d(sK + st * kTileBytes + box * kBoxBytes, &tmKV, &k_full[st], box * 64, bad ? -kPage : (page * 2 * a.Hkv + g) * kPage);
-      if (j >= W::kV && !mbar_wait(&v_empty[st], static_cast<uint32_t>(j / W::kV - 1) & 1u, kWait)) {
-        mbar_wait(&k_full[st], static_cast<uint32_t>(j / W::kK) & 1u, kWait);   // the copies in flight land
-        return false;
-      }
-      ++n_issued;
-      mbar_arrive_expect_tx(&v_full[st], kTileBytes);
-#pragma unroll
-      for (int box = 0; box < 2; ++box)
-        tma_load_2d(sV + st * kTileBytes + box * kBoxBytes, &tmKV, &v_full[st], box * 64,
+        tma_load_2d(sV + vs * kTileBytes + box * kBoxBytes, &tmKV, &v_full[vs], box * 64,
                     bad ? -kPage : ((page * 2 + 1) * a.Hkv + g) * kPage);
     }
     return true;
@@ -299,7 +326,8 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   if (load_thr)
     for (int j = 0; j < min(kAhead, ntile); ++j) request(j);
 
-  // Q into tensor memory, two dims a column: thread (stream x, row r) writes dims 64 x .. of row r
+  // Q into tensor memory, two dims a column (e4m3: four, of its high and then of its low parts): thread (stream x,
+  // row r) writes dims 64 x .. of row r
   const int x = tid >> 7, r = tid & 127;   // softmax threads
   float c = a.scale_log2;                  // the scores' scale to log2 units
   if (softmax_thr) {
@@ -319,26 +347,32 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
       }
-      // 2^-e brings the largest element into [1, 2); zero, subnormal and infinite rows keep e in range
-      const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -126), 126);
+      // 2^(7 - e) brings the largest element into [128, 256); zero and subnormal rows keep e in range
+      const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -119), 126);
       const float ks = a.k_scale[g];
-      const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), ks);   // (the scores' scale stays positive)
-      c = fabsf(ks) * a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      float down = copysignf(__uint_as_float(static_cast<uint32_t>(134 - e) << 23), ks);   // (the scores' scale stays positive)
+      if (big == INFINITY) down = NAN;   // (e4m3 has no infinity)
+      c = fabsf(ks) * a.scale_log2 * __uint_as_float(static_cast<uint32_t>(120 + e) << 23);
+      uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          w[q] = pack16<true>(__uint_as_float(w[q] << 16) * down, __uint_as_float(w[q] & 0xffff0000u) * down);
-        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int i = 0; i < 16; ++i) {
+        const uint4 o = v[i >> 1];
+        const uint32_t w0 = (i & 1) ? o.z : o.x, w1 = (i & 1) ? o.w : o.y;
+        const float q[4] = {__uint_as_float(w0 << 16) * down, __uint_as_float(w0 & 0xffff0000u) * down,
+                            __uint_as_float(w1 << 16) * down, __uint_as_float(w1 & 0xffff0000u) * down};
+        split_e4m3(q, hi[i], lo[i]);
       }
-    }
+      const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kQCol + x * 16;
+      tmem_st16u(at, hi);
+      tmem_st16u(at + 32, lo);
+    } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t w[16] = {v[4 * h].x, v[4 * h].y, v[4 * h].z, v[4 * h].w, v[4 * h + 1].x, v[4 * h + 1].y, v[4 * h + 1].z,
-                              v[4 * h + 1].w, v[4 * h + 2].x, v[4 * h + 2].y, v[4 * h + 2].z, v[4 * h + 2].w, v[4 * h + 3].x,
-                              v[4 * h + 3].y, v[4 * h + 3].z, v[4 * h + 3].w};
-      tmem_st16u(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kQCol + x * 32 + h * 16, w);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w[16] = {v[4 * h].x, v[4 * h].y, v[4 * h].z, v[4 * h].w, v[4 * h + 1].x, v[4 * h + 1].y, v[4 * h + 1].z,
+                                v[4 * h + 1].w, v[4 * h + 2].x, v[4 * h + 2].y, v[4 * h + 2].z, v[4 * h + 2].w, v[4 * h + 3].x,
+                                v[4 * h + 3].y, v[4 * h + 3].z, v[4 * h + 3].w};
+        tmem_st16u(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kQCol + x * 32 + h * 16, w);
+      }
     }
     tmem_wait_st();
   }
@@ -363,7 +397,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     const int y = warp - kSoftmax / 32;
     const bool leader = elect_one();   // the same lane throughout: a commit counts the issuing thread's products
     constexpr uint32_t kKind = kQ8 ? (1u << 4) : (1u << 4) | (1u << 7) | (1u << 10);   // fp32 accumulator; fp16 or bf16
-    constexpr uint32_t idS = kKind | ((static_cast<uint32_t>(kTile) >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t idS = (kQ8 ? 1u << 4 : kKind) | ((static_cast<uint32_t>(kTile) >> 3) << 17) | ((128u >> 4) << 24);   // (e4m3: 0)
     constexpr uint32_t idO = kKind | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);   // B (V) MN-major
     const int mine = ntile > y ? (ntile - y + 1) / 2 : 0;   // tiles of the stream
     const uint32_t s_col = tmem + s_col_of(y), p_col = tmem + p_col_of(y), o_col = tmem + o_col_of(y);
@@ -373,13 +407,17 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     auto s_step = [&](int i) -> bool {
       if (!warp_wait(&k_full[ks], kp) || (i >= 1 && !warp_wait(&s_read[y], static_cast<uint32_t>(i - 1) & 1u))) return false;
       tc_fence_after();
-      const uint64_t d = k_desc + ks * (kTileBytes >> 4);
+      const uint64_t d = k_desc + ks * (W::kKBytes >> 4);
       if (leader) {
+        // 32 bytes of a K row a product; e4m3: the high parts of Q, then the low ones
 #pragma unroll
-        for (int box = 0; box < 2; ++box)
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_ts(s_col, tmem + kQCol + (box * 4 + kk) * 8, d + box * (kBoxBytes >> 4) + 2 * kk, idS, (box > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t q_col = tmem + kQCol + (part * 4 + kk) * 8;
+            if constexpr (kQ8) tc_mma_ts_f8(s_col, q_col, d + 2 * kk, idS, (part > 0 || kk > 0) ? 1u : 0u);
+            else tc_mma_ts(s_col, q_col, d + part * (kBoxBytes >> 4) + 2 * kk, idS, (part > 0 || kk > 0) ? 1u : 0u);
+          }
         tc_commit(&k_empty[ks]);
         tc_commit(&s_full[y]);
       }
@@ -536,43 +574,40 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   } else if constexpr (kQ8) {
     if (tid >= kSoftmax + 96) {
       // ------------------------------------------------------------- e4m3 to fp16 --
-      // four warps for K, four for V; 16 rows at a time, a thread 16 bytes of one
-      const int ct = (tid - (kSoftmax + 96)) & 127, row_of = ct >> 3, ch = ct & 7;
-      const bool v = tid >= kSoftmax + 96 + 128;
-      uint64_t* const empty = v ? v_empty : k_empty;
+      // 16 rows of V at a time, a thread 16 bytes of one
+      const int ct = tid - (kSoftmax + 96), row_of = ct >> 3, ch = ct & 7;
       for (int j = 0; j < ntile && !aborted; ++j) {
-        const int st = j % W::kRaw;   // (as many tiles of each kind)
-          const bool ok = mbar_wait(&raw_full[st], static_cast<uint32_t>(j / W::kRaw) & 1u, kWait) &&
-                          (j < W::kRaw || mbar_wait(&empty[st], static_cast<uint32_t>(j / W::kRaw - 1) & 1u, kWait));
-          if (!__all_sync(0xffffffffu, ok)) {
-            aborted = true;
-            break;
-          }
-          const uint8_t* src = sRaw + (st * 2 + v) * kRawBytes + ch * 16;
-          uint8_t* dst = (v ? sV : sK) + st * kTileBytes + (ch >> 2) * kBoxBytes;
-          const int live = s_bad[st] ? 0 : v ? kv_end - (t_lo + j) * kTile : kTile;   // V rows behind the last key: zeros
+        const int st = j % W::kRaw;   // (as many places as raw ones)
+        if (!warp_wait(&raw_full[st], static_cast<uint32_t>(j / W::kRaw) & 1u) ||
+            (j >= W::kV && !warp_wait(&v_empty[st], static_cast<uint32_t>(j / W::kV - 1) & 1u))) {
+          aborted = true;
+          break;
+        }
+        const uint8_t* src = sRaw + st * kRawBytes + ch * 16;
+        uint8_t* dst = sV + st * kTileBytes + (ch >> 2) * kBoxBytes;
+        const int live = s_bad[st] ? 0 : kv_end - (t_lo + j) * kTile;   // rows behind the last key: zeros
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int row = u * 16 + row_of;
-            uint4 w = *reinterpret_cast<const uint4*>(src + row * 128);
-            if (row >= live) w = make_uint4(0, 0, 0, 0);
-            uint4 h[2];
-            halves_of(w.x, h[0].x, h[0].y);
-            halves_of(w.y, h[0].z, h[0].w);
-            halves_of(w.z, h[1].x, h[1].y);
-            halves_of(w.w, h[1].z, h[1].w);
-            // the 32 bytes are chunks 2 ch and 2 ch + 1 of the box; the upper box's lanes store the odd one first,
-            // so that eight lanes never meet in a bank
-            const int q = (2 * ch) & 7, odd = ch >> 2;
-            *reinterpret_cast<uint4*>(dst + row * 128 + (((q + odd) ^ (row & 7)) << 4)) = odd ? h[1] : h[0];
-            *reinterpret_cast<uint4*>(dst + row * 128 + (((q + 1 - odd) ^ (row & 7)) << 4)) = odd ? h[0] : h[1];
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if ((tid & 31) == 0) {
-            mbar_arrive(v ? &v_full[st] : &k_full[st]);
-            mbar_arrive(&raw_empty[st]);
-          }
+        for (int u = 0; u < 4; ++u) {
+          const int row = u * 16 + row_of;
+          uint4 w = *reinterpret_cast<const uint4*>(src + row * 128);
+          if (row >= live) w = make_uint4(0, 0, 0, 0);
+          uint4 h[2];
+          halves_of(w.x, h[0].x, h[0].y);
+          halves_of(w.y, h[0].z, h[0].w);
+          halves_of(w.z, h[1].x, h[1].y);
+          halves_of(w.w, h[1].z, h[1].w);
+          // the 32 bytes are chunks 2 ch and 2 ch + 1 of the box; the upper box's lanes store the odd one first,
+          // so that eight lanes never meet in a bank
+          const int q = (2 * ch) & 7, odd = ch >> 2;
+          *reinterpret_cast<uint4*>(dst + row * 128 + (((q + odd) ^ (row & 7)) << 4)) = odd ? h[1] : h[0];
+          *reinterpret_cast<uint4*>(dst + row * 128 + (((q + 1 - odd) ^ (row & 7)) << 4)) = odd ? h[0] : h[1];
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if ((tid & 31) == 0) {
+          mbar_arrive(&v_full[st]);
+          mbar_arrive(&raw_empty[st]);
+        }
       }
       if (aborted) {
         *s_abort = 1;
@@ -585,12 +620,9 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   __syncthreads();   // every product is done; loads too, unless a wait ran out
   if (load_thr && *s_abort) {   // the copies still in flight land before the rings are overlaid
     for (int t = max(0, n_issued - W::kK); t < n_issued; ++t) {
-      if constexpr (kQ8) {
-        mbar_wait(&raw_full[t % W::kRaw], static_cast<uint32_t>(t / W::kRaw) & 1u, kWait);
-      } else {
-        mbar_wait(&k_full[t % W::kK], static_cast<uint32_t>(t / W::kK) & 1u, kWait);
-        mbar_wait(&v_full[t % W::kV], static_cast<uint32_t>(t / W::kV) & 1u, kWait);
-      }
+      mbar_wait(&k_full[t % W::kK], static_cast<uint32_t>(t / W::kK) & 1u, kWait);
+      if constexpr (kQ8) mbar_wait(&raw_full[t % W::kRaw], static_cast<uint32_t>(t / W::kRaw) & 1u, kWait);
+      else mbar_wait(&v_full[t % W::kV], static_cast<uint32_t>(t / W::kV) & 1u, kWait);
     }
   }
   __syncthreads();
@@ -731,7 +763,7 @@ WideKernel wide_kernel(int share) {
 }
 int bytes_of(int share) { return share ? wide_bytes<__nv_bfloat16>() : wide_bytes<__nv_fp8_storage_t>(); }
 int threads_of(int share) { return share ? Wide<__nv_bfloat16>::kThreads : Wide<__nv_fp8_storage_t>::kThreads; }
-static_assert(8 * kTileBytes >= (128 * 128 + 256) * 4, "the partials overlay the rings");
+static_assert(6 * kRawBytes + 4 * kTileBytes >= (128 * 128 + 256) * 4, "the partials overlay the rings");
 
 // Clusters of S CTAs that can be resident at once (asked once per device and S).
 cudaError_t wide_capacity(int share, int S, int sms, int* n) {

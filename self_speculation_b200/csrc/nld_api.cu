@@ -70,6 +70,20 @@ bool make_map_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t 
   return r == CUDA_SUCCESS;
 }
 
+// The same over rows of 128 bytes (the e4m3 pool): a box is box_rows whole rows.
+bool make_map_u8(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
+  EncodeTiledFn enc = get_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {128, rows};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // Tensor map over a pre-tiled weight matrix: a 2D view [row_tiles * (K/64) * 128 rows, 64
 // elements] whose box {64, 128} is one contiguous 16 KB block.
 bool make_map_tiled(CUtensorMap* map, const void* base, int n_rows, int K) {
@@ -2319,8 +2333,10 @@ nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float*
     AttnWideArgs a{};
     fill(a);
     if ((static_cast<long long>(m) * G + 127) / 128 * batch > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
-    const CUtensorMap none{};
-    if ((e = attn_wide_plan(batch, max_len, sms, a)) == cudaSuccess) e = launch_attention_wide(st, &none, a, batch, false);
+    CUtensorMap map;
+    if (!make_map_u8(&map, d_kv_pool, static_cast<uint64_t>(n_pages) * 2 * n_kv_heads * kPage, kPage))
+      return fail(nullptr, NLD_ERR_CUDA, "tensor map encode failed (pool)");
+    if ((e = attn_wide_plan(batch, max_len, sms, a)) == cudaSuccess) e = launch_attention_wide(st, &map, a, batch, false);
   }
   if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
   return NLD_OK;
