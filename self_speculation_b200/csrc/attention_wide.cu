@@ -15,19 +15,19 @@
 // core), and 512 more if Q had to be read for every S.  The streams' partials meet in shared memory at the end,
 // those of the KV splits over the cluster's distributed shared memory, in a fixed order.
 //
-// What it measured: two pages of 128 rows take 1850 cycles, 55 % of the exponential unit; the rest is the latency of a
-// softmax thread's steps (scores in 85 cycles, maximum 175, exponentials 512 to 800, waits 370, P out 100).  Two threads a
-// row (sixteen softmax warps) took 10 to 17 % longer, a quarter of the exponentials as polynomials on the multiply-add
-// pipe 1 to 6 %, the maximum taken beside the exponentials of a stale one the same time.  A CTA's fixed cost is 9 us
-// (Q 2, partials 2, merge 3.5), which few pages a CTA do not hide.
+// What it measured (8 sequences of 16416 keys, 32 rows, 32 / 8 heads, e4m3: 90 us, 0.76 PFLOP/s): two pages of 128 rows take
+// 1850 cycles, 55 % of the exponential unit; the rest is the latency of a softmax thread's steps (scores in 85 cycles,
+// maximum 175, exponentials 512 to 800, waits 370, P out 100).  Two threads a row (sixteen softmax warps) took 10 to
+// 17 % longer, a quarter of the exponentials as polynomials on the multiply-add pipe 1 to 6 %, the next page's scores
+// fetched under this one's exponentials 9 %, the maximum taken beside the exponentials of a stale one the same time.
+// A CTA's fixed cost is 9 us (Q 2, partials 2, merge 3.5), which few pages a CTA do not hide.
 //
-// bf16: K and V come by TMA into rings of six pages.  e4m3: a page's K (or V) rows of a kv head are 8 KB in a
-// row and come by bulk copies; eight warps (four for K, four for V) turn them into fp16 tiles (exact), four of K and
-// four of V, in the swizzled layout of the descriptors.  (Four warps for both were the bottleneck, 166 us where
-// eight take 103; moving the bits by integer operations instead of the cvt, 141.)  K's place frees when S is done,
-// V's when O is.  Q's rows are scaled by a power of two into fp16's range there, and P is rounded to fp16
-// (attention_small.cu has the errors); over the bf16 cache P is rounded to bf16.  The maximum that exponents refer to moves only when it has grown by 2^8, so O is
-// rarely rescaled; sums, maxima and O are in fp32.
+// bf16: K and V come by TMA into rings of six pages.  e4m3: K's page goes to the tensor core as it comes (kind::f8f6f4)
+// against Q in two e4m3 parts (split_e4m3); V's comes by bulk copies, and four warps turn it into an fp16 tile (exact)
+// in the swizzled layout of the descriptors, for P rounded to fp16 (attention_small.cu has that error).  Converting K
+// as well took 95 us with eight warps and 166 with four; by integer operations instead of the cvt, 141 with eight.
+// K's place frees when S is done, V's when O is.  Over the bf16 cache P is rounded to bf16.  The maximum that exponents
+// refer to moves only when it has grown by 2^8, so O is rarely rescaled; sums, maxima and O are in fp32.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -165,7 +165,9 @@ NLD_DEV bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
   return p != 0;
 }
-// Four numbers as e4m3, and what that leaves of them as e4m3.
+// Four numbers below 256 of a row whose largest is 128 or more, as e4m3, and what that leaves of them as e4m3: of bf16's eight
+// bits the first takes four, rounded, and the second the rest.  Exact from 2^-9 of the row's largest element on; below, where
+// the second is subnormal in steps of 2^-9, off by at most 2^-17 of that element.
 NLD_DEV void split_e4m3(const float (&q)[4], uint32_t& hi, uint32_t& lo) {
   hi = lo = 0;
 #pragma unroll

@@ -6,6 +6,7 @@ import torch
 
 import test_gpu_attention_q8 as q8
 import test_gpu_attention_shared as shared
+from oracle import operators as oop
 
 pytestmark = pytest.mark.gpu
 
@@ -63,6 +64,22 @@ def test_wide_queries_of_any_size(size):
     s = q8.make([70], 20, 8, 2, seed=4, kscale=1.0 / size)
     s["q"] = (s["q"].float() * size).to(torch.bfloat16)
     q8.check(s, q8.run(s, 1), 1)
+
+
+@pytest.mark.parametrize("size", [2.0 ** 7, 2.0 ** 9, 2.0 ** 12])
+def test_wide_queries_with_a_large_element(size):
+    """A row's elements below 2^-9 of its largest may each be off by 2^-17 of it: the scores by
+    max|q| 2^-17 sum |k| scale."""
+    s = q8.make([300], 20, 8, 2, seed=5, kscale=1.0 / size)
+    s["q"][..., 77] = torch.copysign(torch.full((), size), s["q"][..., 77].float()).to(torch.bfloat16)
+    out = q8.run(s, 1)[0].double()
+    k, v = oop.paged_rows(s["pool"], s["table"][0].tolist(), 320)
+    k, v = k * s["ks"].double()[:, None], v * s["vs"].double()[:, None]
+    q, scale = s["q"][0].double(), 128 ** -0.5
+    want = oop.block_causal_attention(s["q"][0], k, v, 1)
+    off = q.abs().max().item() * 2.0 ** -17 * k.abs().sum(-1).max().item() * scale
+    tol = q8.tolerance(q, k, v, want, scale, 2.0 ** -11, 1.0) + 2 * v.abs().max().item() * off
+    assert ((out - want).abs() <= tol).all()
 
 
 @pytest.mark.parametrize("m", [1, 40])
