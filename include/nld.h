@@ -510,7 +510,8 @@ nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float*
  *                   from the end of the prefix: its slot 0 holds position shared_len (the
  *                   position_offset of nld_qk_norm_rope).
  *   d_workspace     16-byte aligned, nld_attention_shared_workspace_size() bytes: the prefix's fp32
- *                   partial of every (row, query head).  Calls sharing it must not overlap.
+ *                   partials of every (row, query head), one or several.  Calls sharing it must not
+ *                   overlap.
  *   d_err           one int32 or NULL: a lens[b] outside 0..pages_per_seq*64-m is clamped, a page id
  *                   outside the pool reads as zeros, and NLD_DEVERR_KV_OVERFLOW is or-ed in;
  *                   NLD_DEVERR_TIMEOUT if a bounded wait ran out.

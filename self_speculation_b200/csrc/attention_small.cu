@@ -433,8 +433,16 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
     const int row = rt * kR + r;
     const int pos = row / a.G;
     const size_t at = (static_cast<size_t>(b) * a.m + pos) * a.Hq + static_cast<size_t>(g) * a.G + (row - pos * a.G);
-    if constexpr (kShare != 0)
-      if (share_merge<kShare>(a.part_o, a.part_ml, at, lane, M, L, v)) return;
+    if constexpr (kShare == kPrefixPass) {
+      reinterpret_cast<float4*>(a.part.o)[at * 32 + lane] = v;
+      if (lane == 0) a.part.ml[at] = make_float2(M, L);
+      return;
+    }
+    if constexpr (kShare == kOwnPass)
+      if (a.part.o != nullptr) {
+        if (a.part.per) share_add_runs(a.part, g, b * a.m * a.G + row, lane, M, L, v);
+        else share_add(a.part.ml[at], reinterpret_cast<const float4*>(a.part.o)[at * 32 + lane], M, L, v);
+      }
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at * 128;
     const float k = vs / L;   // a row sees its own key at least
     const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * k, v.y * k), hi = __floats2bfloat162_rn(v.z * k, v.w * k);

@@ -15,12 +15,19 @@
 // core), and 512 more if Q had to be read for every S.  The streams' partials meet in shared memory at the end,
 // those of the KV splits over the cluster's distributed shared memory, in a fixed order.
 //
-// What it measured (8 sequences of 16416 keys, 32 rows, 32 / 8 heads, e4m3: 90 us, 0.76 PFLOP/s): two pages of 128 rows take
+// What it measured (8 sequences of 16416 keys, 32 rows, 32 / 8 heads, e4m3: 88 us, 0.78 PFLOP/s; back to back
+// for longer the power limit takes the clock to 1.7 GHz, and that 102): two pages of 128 rows take
 // 1850 cycles, 55 % of the exponential unit; the rest is the latency of a softmax thread's steps (scores in 85 cycles,
 // maximum 175, exponentials 512 to 800, waits 370, P out 100).  Two threads a row (sixteen softmax warps) took 10 to
 // 17 % longer, a quarter of the exponentials as polynomials on the multiply-add pipe 1 to 6 %, the next page's scores
 // fetched under this one's exponentials 9 %, the maximum taken beside the exponentials of a stale one the same time.
-// A CTA's fixed cost is 9 us (Q 2, partials 2, merge 3.5), which few pages a CTA do not hide.
+// A CTA's fixed cost is 8 us (Q 2, partials 1, merge 3.5), which few pages a CTA do not hide.
+//
+// A prefix pass may have more query tiles than SMs, and then a round of clusters that few of them fill.  Where it costs less,
+// it is cut into runs of pages (kRuns): a CTA an SM takes as many pages as any other, across query tiles.  Each tile's part
+// goes to the workspace as it lies in shared memory, by a copy beside which the next part starts, and the own pass adds
+// the parts of a row in their order.  16 sequences x 32 rows of 40 / 8 heads over 4133 shared and 300 own keys: 97 -> 82 us;
+// 20 x 32 rows of 32 / 8 heads over 6000: 120 -> 100; 64 rows a kv head over 16384, in clusters: 47.
 //
 // bf16: K and V come by TMA into rings of six pages.  e4m3: K's page goes to the tensor core as it comes (kind::f8f6f4)
 // against Q in two e4m3 parts (split_e4m3); V's comes by bulk copies, and four warps turn it into an fp16 tile (exact)
@@ -187,13 +194,22 @@ NLD_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar
                : "memory");
 }
 
+NLD_DEV void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(smem_u32(src)),
+               "r"(bytes)
+               : "memory");
+}
+NLD_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+NLD_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }   // the source is free
+NLD_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }             // the copies are done
+
 // Columns of tensor memory.
 NLD_DEV constexpr uint32_t s_col_of(int stream) { return stream * 96; }
 NLD_DEV constexpr uint32_t p_col_of(int stream) { return stream * 96 + 64; }
 NLD_DEV constexpr uint32_t o_col_of(int stream) { return 192 + stream * 128; }
 constexpr uint32_t kQCol = 448;
 
-template <typename E, int kShare>
+template <typename E, int kShare, bool kRuns>
 __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     attn_wide_kernel(const __grid_constant__ CUtensorMap tmKV, const AttnWideArgs a) {
   using W = Wide<E>;
@@ -220,10 +236,11 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   int* s_bad = reinterpret_cast<int*>(bars + 47);   // [kRaw] the page is outside the pool
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform for the compiler too)
-  const int split = blockIdx.x, g = blockIdx.y;
-  const int b = blockIdx.z / a.q_tiles, qt = blockIdx.z - b * a.q_tiles;
+  const int split = blockIdx.x;
+  int g = blockIdx.y;
+  const int b = blockIdx.z / a.q_tiles;
   const int all = a.m * a.G;                              // rows of the (sequence, kv head)
-  const int r0 = qt * a.rows, rows = min(a.rows, all - r0);   // of this CTA
+  int r0 = (blockIdx.z - b * a.q_tiles) * a.rows, rows = min(a.rows, all - r0);   // of this CTA
   const bool softmax_thr = tid < kSoftmax;
   const bool issue_warp = warp == kSoftmax / 32 || warp == kSoftmax / 32 + 1;
   const bool load_thr = tid == kSoftmax + 64;
@@ -275,8 +292,29 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   const int kv_end = seen_by(r0 + rows - 1);   // the last row sees the most
   const int n_pages = (kv_end + kPage - 1) / kPage;
   const int per = (n_pages + a.S - 1) / a.S;
-  const int t_lo = split * per;
-  const int ntile = max(0, min(n_pages, t_lo + per) - t_lo);
+  int t_lo = split * per;
+  int ntile = max(0, min(n_pages, t_lo + per) - t_lo);
+  // The prefix pass: pages [at, end) of all its (kv head, query tile, page), a query tile's part at a time.  The
+  // rings and the barriers run on from one part to the next: done tiles of the CTA, of each stream.
+  unsigned at_page = 0, end_page = 0;
+  size_t place = 0;
+  int done = 0, done_0 = 0, done_1 = 0, part = 0;
+  constexpr bool runs = kShare == kPrefixPass && kRuns;
+  if constexpr (runs) {
+    at_page = split * a.part.per;
+    end_page = min(at_page + a.part.per, static_cast<unsigned>(a.Hkv * a.q_tiles) * n_pages);
+  }
+  auto next_part = [&] {
+    const int u = at_page / static_cast<unsigned>(n_pages);
+    g = u / a.q_tiles;
+    r0 = (u - g * a.q_tiles) * a.rows;
+    rows = min(a.rows, all - r0);
+    t_lo = at_page - u * n_pages;
+    // (uniform for the compiler too)
+    ntile = __shfl_sync(0xffffffffu, min(n_pages - t_lo, static_cast<int>(end_page - at_page)), 0);
+    place = static_cast<size_t>(u + split) * 128;
+  };
+  if constexpr (runs) next_part();
 
   tc_fence_before();
   __syncthreads();
@@ -290,6 +328,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     const int page = table[t_lo + j];
     const bool bad = page < 0 || page >= a.n_pages;
     if (bad) set_err(a.err, NLD_DEVERR_KV_OVERFLOW);
+    j += done;
     const int ks = j % W::kK;
     if (j >= W::kK && !mbar_wait(&k_empty[ks], static_cast<uint32_t>(j / W::kK - 1) & 1u, kWait)) return false;
     // (a page outside the pool: rows outside the tensor, which read as zeros)
@@ -325,9 +364,14 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   // e4m3: the first tiles come while Q is laid out (97 -> 95 us; over bf16 pages, without a conversion behind them, the
   // block of 32 with a shared prefix took 104 us that way and 98 without)
   constexpr int kAhead = kQ8 ? W::kRaw : 0;
+  bool aborted = false;
+  float m_ref, l_sum;
+  for (;;) {   // (a part of the prefix pass at a time; else once)
+  m_ref = -INFINITY;
+  l_sum = 0.f;
+  const int ahead = part > 0 ? min(W::kK, ntile) : min(kAhead, ntile);
   if (load_thr)
-    for (int j = 0; j < min(kAhead, ntile); ++j) request(j);
-
+    for (int j = 0; j < ahead && !aborted; ++j) aborted = !request(j);
   // Q into tensor memory, two dims a column (e4m3: four, of its high and then of its low parts): thread (stream x,
   // row r) writes dims 64 x .. of row r
   const int x = tid >> 7, r = tid & 127;   // softmax threads
@@ -381,13 +425,12 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if constexpr (kShare == kPrefixPass) pdl_launch_dependents();
+  if constexpr (kShare == kPrefixPass)
+    if (part == 0) pdl_launch_dependents();
 
-  bool aborted = false;
-  float m_ref = -INFINITY, l_sum = 0.f;
   if (load_thr) {
     // ---------------------------------------------------------------- loads --
-    for (int j = kAhead; j < ntile && !aborted; ++j) aborted = !request(j);
+    for (int j = ahead; j < ntile && !aborted; ++j) aborted = !request(j);
     if (aborted) {
       *s_abort = 1;
       set_err(a.err, NLD_DEVERR_TIMEOUT);
@@ -404,10 +447,11 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     const int mine = ntile > y ? (ntile - y + 1) / 2 : 0;   // tiles of the stream
     const uint32_t s_col = tmem + s_col_of(y), p_col = tmem + p_col_of(y), o_col = tmem + o_col_of(y);
     const uint64_t k_desc = sdesc_k_sw128(smem_u32(sK)), v_desc = desc_mn(smem_u32(sV), kBoxBytes, 1024);
-    int ks = y, kp = 0, vs = y, vp = 0;   // stage and parity of the stream's next K and V
+    const int first = y ? done_1 : done_0;   // tiles of the stream in earlier parts
+    int ks = (done + y) % W::kK, kp = ((done + y) / W::kK) & 1, vs = (done + y) % W::kV, vp = ((done + y) / W::kV) & 1;   // stage and parity of the stream's next K and V
     // S of the stream's tile i, once the softmax has read that of tile i - 1
     auto s_step = [&](int i) -> bool {
-      if (!warp_wait(&k_full[ks], kp) || (i >= 1 && !warp_wait(&s_read[y], static_cast<uint32_t>(i - 1) & 1u))) return false;
+      if (!warp_wait(&k_full[ks], kp) || (i >= 1 && !warp_wait(&s_read[y], static_cast<uint32_t>(first + i - 1) & 1u))) return false;
       tc_fence_after();
       const uint64_t d = k_desc + ks * (W::kKBytes >> 4);
       if (leader) {
@@ -433,7 +477,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     };
     if (mine > 0) aborted = !s_step(0);
     for (int i = 0; i < mine && !aborted; ++i) {
-      if ((i + 1 < mine && !s_step(i + 1)) || !warp_wait(&p_full[y], static_cast<uint32_t>(i) & 1u) || !warp_wait(&v_full[vs], vp)) {
+      if ((i + 1 < mine && !s_step(i + 1)) || !warp_wait(&p_full[y], static_cast<uint32_t>(first + i) & 1u) || !warp_wait(&v_full[vs], vp)) {
         aborted = true;
         break;
       }
@@ -460,7 +504,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     // every product of this warp is done before tensor memory is released
     if (leader) {
       tc_commit(fin);
-      mbar_wait(fin, 0, kWait);
+      mbar_wait(fin, part & 1, kWait);
     }
     __syncwarp();
   } else if (softmax_thr) {
@@ -470,10 +514,11 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     const uint32_t s_at = tmem + lane + s_col_of(x), p_at = tmem + lane + p_col_of(x), o_at = tmem + lane + o_col_of(x);
     const f2 c2 = pair(c, c);
     const int mine = ntile > x ? (ntile - x + 1) / 2 : 0;   // tiles of the stream
+    const int first = x ? done_1 : done_0;
     for (int i = 0; i < mine; ++i) {
       const int j = x + 2 * i;
       // tcgen05.ld / st are for whole warps: every exit of this loop is taken by the warp together
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], static_cast<uint32_t>(i) & 1u, kWait))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], static_cast<uint32_t>(first + i) & 1u, kWait))) {
         aborted = true;
         break;
       }
@@ -499,7 +544,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       const bool move = mx > m_ref + kMove;
       const bool scale_o = move && m_ref != -INFINITY;
       if (__any_sync(0xffffffffu, scale_o)) {   // (i > 0: m_ref was set)
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(i - 1) & 1u, kWait))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(first + i - 1) & 1u, kWait))) {
           aborted = true;
           break;
         }
@@ -536,7 +581,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
         }
       }
       // P is free once O += P V of the tile before has read it
-      if (i >= 1 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(i - 1) & 1u, kWait))) {
+      if (i >= 1 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(first + i - 1) & 1u, kWait))) {
         aborted = true;
         break;
       }
@@ -551,8 +596,8 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
         // V rows behind the last key: P is 0 there, V may be anything
         const int dead = (t_lo + j + 1) * kTile - kv_end;
         if (dead > 0) {
-          const int vs = j % W::kV;
-          if (!__all_sync(0xffffffffu, mbar_wait(&v_full[vs], static_cast<uint32_t>(j / W::kV) & 1u, kWait))) {
+          const int vs = (done + j) % W::kV;
+          if (!__all_sync(0xffffffffu, mbar_wait(&v_full[vs], static_cast<uint32_t>((done + j) / W::kV) & 1u, kWait))) {
             aborted = true;
             break;
           }
@@ -566,7 +611,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       __syncwarp();
       if ((tid & 31) == 0) mbar_arrive(&p_full[x]);
     }
-    if (!aborted && mine > 0 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(mine - 1) & 1u, kWait)))
+    if (!aborted && mine > 0 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(first + mine - 1) & 1u, kWait)))
       aborted = true;
     if (aborted) {
       *s_abort = 1;
@@ -629,55 +674,76 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   }
   __syncthreads();
   float* sO = reinterpret_cast<float*>(smem);   // [128][128]; float4 s of row r at s ^ (r % 32)
-  float* sML = sO + 128 * 128;                  // [128][2] max, sum
-  const bool have = softmax_thr && ntile > x && !*s_abort;
-  const uint32_t o_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + o_col_of(x & 1);
-  // stream 0 leaves its row, stream 1 adds its own
-  auto leave = [&](bool add) {
-    float w0 = 0.f, w1 = have ? 1.f : 0.f, M = have ? m_ref : -INFINITY, L = have ? l_sum : 0.f;
-    if (add) {
-      const float2 ml = *reinterpret_cast<const float2*>(sML + 2 * r);
-      const float top = fmaxf(M, ml.x);
-      w0 = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-      w1 = M == -INFINITY ? 0.f : exp2f(M - top);
-      M = top;
-      L = w0 * ml.y + w1 * L;
-    }
-    const bool take = __any_sync(0xffffffffu, w1 != 0.f);   // (a stream without a tile has no O)
-#pragma unroll 2
-    for (int u = 0; u < 4; ++u) {
-      uint32_t o[32];
-      if (take) {
-        tmem_ld32_nowait(o_at + u * 32, o);
-        tmem_wait_ld(o);
-      } else {
+  float2* sML = reinterpret_cast<float2*>(sO + 128 * 128);   // [128] max, sum
+  float2* sX = sML + 128;                       // [stream][128] the streams'
+  unsigned* sAt = reinterpret_cast<unsigned*>(sX + 256);   // [2][128] places of the prefix's parts, their numbers
+  if (softmax_thr) {
+    const bool have = ntile > x && !*s_abort;
+    sX[tid] = have ? make_float2(m_ref, l_sum) : make_float2(-INFINITY, 0.f);
+  }
+  __syncthreads();
+  // a thread adds dims 64 x .. of both streams' rows r
+  if (softmax_thr) {
+    const float2 ml0 = sX[r], ml1 = sX[128 + r];
+    const float M = fmaxf(ml0.x, ml1.x);
+    const float w0 = ml0.x == -INFINITY ? 0.f : exp2f(ml0.x - M), w1 = ml1.x == -INFINITY ? 0.f : exp2f(ml1.x - M);
+    // (a stream without a tile has no O)
+    const bool take0 = __any_sync(0xffffffffu, w0 != 0.f), take1 = __any_sync(0xffffffffu, w1 != 0.f);
+    const uint32_t lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * 64;
+#pragma unroll 1
+    for (int u = 0; u < 2; ++u) {
+      uint32_t o0[32], o1[32];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = 0u;
-      }
+      for (int k = 0; k < 32; ++k) o0[k] = o1[k] = 0u;
+      if (take0) tmem_ld32_nowait(lane + o_col_of(0) + u * 32, o0);
+      if (take1) tmem_ld32_nowait(lane + o_col_of(1) + u * 32, o1);
+      tmem_wait_ld(o0);
+      tmem_wait_ld(o1);
 #pragma unroll
       for (int k = 0; k < 32; k += 4) {
-        float4* at = reinterpret_cast<float4*>(sO + r * 128 + (((u * 8 + (k >> 2)) ^ (r & 31)) << 2));
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w0 != 0.f)
+          v = make_float4(__uint_as_float(o0[k]) * w0, __uint_as_float(o0[k + 1]) * w0, __uint_as_float(o0[k + 2]) * w0,
+                          __uint_as_float(o0[k + 3]) * w0);
         if (w1 != 0.f)
-          v = make_float4(__uint_as_float(o[k]) * w1, __uint_as_float(o[k + 1]) * w1, __uint_as_float(o[k + 2]) * w1,
-                          __uint_as_float(o[k + 3]) * w1);
-        if (add && w0 != 0.f) {
-          const float4 z = *at;
-          v = make_float4(fmaf(z.x, w0, v.x), fmaf(z.y, w0, v.y), fmaf(z.z, w0, v.z), fmaf(z.w, w0, v.w));
-        }
-        *at = v;
+          v = make_float4(fmaf(__uint_as_float(o1[k]), w1, v.x), fmaf(__uint_as_float(o1[k + 1]), w1, v.y),
+                          fmaf(__uint_as_float(o1[k + 2]), w1, v.z), fmaf(__uint_as_float(o1[k + 3]), w1, v.w));
+        *reinterpret_cast<float4*>(sO + r * 128 + (((x * 16 + u * 8 + (k >> 2)) ^ (r & 31)) << 2)) = v;
       }
     }
-    *reinterpret_cast<float2*>(sML + 2 * r) = make_float2(M, L);
-  };
-  if (softmax_thr && x == 0) leave(false);
-  __syncthreads();
-  if (softmax_thr && x == 1) leave(true);
+    if (x == 0) sML[r] = make_float2(M, w0 * ml0.y + w1 * ml1.y);
+    if constexpr (runs) fence_proxy_async();
+    if constexpr (kShare == kOwnPass && kRuns)
+      if (x == 1 && r < rows) {
+        unsigned first;
+        sAt[128 + r] = share_places(a.part, g, b * all + r0 + r, first);
+        sAt[r] = first;
+      }
+  }
   tc_fence_before();
   __syncthreads();
-  if (warp == kSoftmax / 32) {
+  const bool last = !runs || at_page + ntile >= end_page || *s_abort;
+  if (last && warp == kSoftmax / 32) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+
+  if constexpr (runs) {   // a part is left as it lies here, by a copy that only the next part's loads wait for
+    if (load_thr) {
+      bulk_store(a.part.o + place * 128, sO, 128 * 128 * 4);
+      bulk_store(a.part.ml + place, sML, 128 * 8);
+      bulk_commit();
+      if (last) bulk_wait();
+      else bulk_wait_read();
+    }
+    if (last) break;
+    at_page += ntile;
+    done = __shfl_sync(0xffffffffu, done + ntile, 0);
+    done_0 = __shfl_sync(0xffffffffu, done_0 + (ntile + 1) / 2, 0);
+    done_1 = __shfl_sync(0xffffffffu, done_1 + ntile / 2, 0);
+    ++part;
+    next_part();
+    continue;
   }
 
   // the splits' partials: rank q of the cluster finishes rows q, q + S, .., a warp four at a time (one row at a
@@ -692,7 +758,8 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   const uint32_t o_base = smem_u32(sO), ml_base = smem_u32(sML);
   constexpr int kRows = 4;
   for (int t0 = warp * kRows; rank + t0 * S < rows; t0 += W::kThreads / 32 * kRows) {
-    size_t at[kRows];   // token x query head
+    size_t at[kRows], pre_at[kRows];   // token x query head; the prefix's first part
+    int pre_n[kRows];
     float2 ml[kRows], pre_ml[kRows];
     float4 acc[kRows], pre[kRows];
 #pragma unroll
@@ -703,9 +770,11 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       // (max, sum) of split q in lane q
       ml[i] = d4 < S ? ld_dsmem_f2((S > 1 ? dsmem_addr(ml_base, d4) : ml_base) + rr * 8) : make_float2(-INFINITY, 0.f);
       if constexpr (kShare == kOwnPass)
-        if (a.part_o != nullptr) {
-          pre_ml[i] = a.part_ml[at[i]];
-          pre[i] = reinterpret_cast<const float4*>(a.part_o)[at[i] * 32 + d4];
+        if (a.part.o != nullptr) {
+          pre_at[i] = kRuns ? sAt[rr] : at[i];
+          if constexpr (kRuns) pre_n[i] = sAt[128 + rr];
+          pre_ml[i] = a.part.ml[pre_at[i]];
+          pre[i] = kRuns ? *share_at(a.part, pre_at[i], d4) : reinterpret_cast<const float4*>(a.part.o)[at[i] * 32 + d4];
         }
       acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -739,53 +808,80 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
           }
         }
       }
+    if constexpr (kShare == kOwnPass && kRuns) {   // a part of each row at a time
+      int most = 1;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        share_add(pre_ml[i], pre[i], M[i], L[i], acc[i]);
+        most = max(most, pre_n[i]);
+      }
+      for (int n = 1; n < most; ++n) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const size_t to = pre_at[i] + min(n, pre_n[i] - 1) * 128;
+          pre_ml[i] = a.part.ml[to];
+          pre[i] = *share_at(a.part, to, d4);
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (n < pre_n[i]) share_add(pre_ml[i], pre[i], M[i], L[i], acc[i]);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       if (rank + (t0 + i) * S >= rows) break;
       if constexpr (kShare == kPrefixPass) {
-        reinterpret_cast<float4*>(a.part_o)[at[i] * 32 + d4] = acc[i];
-        if (d4 == 0) a.part_ml[at[i]] = make_float2(M[i], L[i]);
+        reinterpret_cast<float4*>(a.part.o)[at[i] * 32 + d4] = acc[i];
+        if (d4 == 0) a.part.ml[at[i]] = make_float2(M[i], L[i]);
         continue;
       }
       if constexpr (kShare == kOwnPass)
-        if (a.part_o != nullptr) share_add(pre_ml[i], pre[i], M[i], L[i], acc[i]);
+        if (!kRuns && a.part.o != nullptr) share_add(pre_ml[i], pre[i], M[i], L[i], acc[i]);
       const float k = L[i] > 0.f ? vscale / L[i] : 0.f;
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at[i] * 128 + 4 * d4) =
           make_uint2(pack16<false>(acc[i].x * k, acc[i].y * k), pack16<false>(acc[i].z * k, acc[i].w * k));
     }
   }
-  if (S > 1) cluster_sync();   // peers may still be reading this CTA's shared memory
+  break;
+  }
+  if (a.S > 1) cluster_sync();   // peers may still be reading this CTA's shared memory
 }
 
 using WideKernel = void (*)(const CUtensorMap, const AttnWideArgs);
-WideKernel wide_kernel(int share) {
-  if (share == kPrefixPass) return attn_wide_kernel<__nv_bfloat16, kPrefixPass>;
-  if (share == kOwnPass) return attn_wide_kernel<__nv_bfloat16, kOwnPass>;
-  return attn_wide_kernel<__nv_fp8_storage_t, 0>;
+// Kinds of kernels: e4m3, own pass, prefix pass; these two with a prefix pass in runs of pages
+int kind_of(const AttnWideArgs& a) { return a.share && a.part.per ? a.share + 2 : a.share; }
+WideKernel wide_kernel(int kind) {
+  switch (kind) {
+    case kOwnPass: return attn_wide_kernel<__nv_bfloat16, kOwnPass, false>;
+    case kPrefixPass: return attn_wide_kernel<__nv_bfloat16, kPrefixPass, false>;
+    case kOwnPass + 2: return attn_wide_kernel<__nv_bfloat16, kOwnPass, true>;
+    case kPrefixPass + 2: return attn_wide_kernel<__nv_bfloat16, kPrefixPass, true>;
+  }
+  return attn_wide_kernel<__nv_fp8_storage_t, 0, false>;
 }
-int bytes_of(int share) { return share ? wide_bytes<__nv_bfloat16>() : wide_bytes<__nv_fp8_storage_t>(); }
-int threads_of(int share) { return share ? Wide<__nv_bfloat16>::kThreads : Wide<__nv_fp8_storage_t>::kThreads; }
+int bytes_of(int kind) { return kind ? wide_bytes<__nv_bfloat16>() : wide_bytes<__nv_fp8_storage_t>(); }
+int threads_of(int kind) { return kind ? Wide<__nv_bfloat16>::kThreads : Wide<__nv_fp8_storage_t>::kThreads; }
 static_assert(6 * kRawBytes + 4 * kTileBytes >= (128 * 128 + 256) * 4, "the partials overlay the rings");
 
 // Clusters of S CTAs that can be resident at once (asked once per device and S).
-cudaError_t wide_capacity(int share, int S, int sms, int* n) {
-  static int cache[16][3][9];
+cudaError_t wide_capacity(int kind, int S, int sms, int* n) {
+  static int cache[16][5][9];
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
-  int* c = dev < 16 ? &cache[dev][share][S] : nullptr;
+  int* c = dev < 16 ? &cache[dev][kind][S] : nullptr;
   if (c && *c) {
     *n = *c;
     return cudaSuccess;
   }
-  if ((e = cudaFuncSetAttribute(wide_kernel(share), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes_of(share))) != cudaSuccess)
+  if ((e = cudaFuncSetAttribute(wide_kernel(kind), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes_of(kind))) != cudaSuccess)
     return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(S * (sms / S));
-  cfg.blockDim = dim3(threads_of(share));
-  cfg.dynamicSmemBytes = bytes_of(share);
+  cfg.blockDim = dim3(threads_of(kind));
+  cfg.dynamicSmemBytes = bytes_of(kind);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = S;
@@ -793,7 +889,7 @@ cudaError_t wide_capacity(int share, int S, int sms, int* n) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaOccupancyMaxActiveClusters(n, wide_kernel(share), &cfg)) != cudaSuccess) return e;
+  if ((e = cudaOccupancyMaxActiveClusters(n, wide_kernel(kind), &cfg)) != cudaSuccess) return e;
   *n = std::max(1, *n);
   if (c) *c = *n;
   return cudaSuccess;
@@ -812,7 +908,7 @@ cudaError_t attn_wide_plan(int batch, int max_len, int sms, AttnWideArgs& a) {
   double best = 0;
   for (int S = 1; S <= 8 && S <= tiles; ++S) {
     int cap = 1;
-    const cudaError_t e = wide_capacity(a.share, S, sms, &cap);
+    const cudaError_t e = wide_capacity(kind_of(a), S, sms, &cap);
     if (e != cudaSuccess) return e;
     const double cost = static_cast<double>((units + cap - 1) / cap) * ((tiles + S - 1) / S + 16.0);
     if (S == 1 || cost < best) {
@@ -820,14 +916,30 @@ cudaError_t attn_wide_plan(int batch, int max_len, int sms, AttnWideArgs& a) {
       a.S = S;
     }
   }
+  if (a.share == kPrefixPass && units * tiles <= INT32_MAX) {
+    // Or runs of pages: their parts' rest is 12 (the next part starts beside it), and the own pass reads more: 10, and 2 for
+    // each part of a tile.
+    const int ctas = std::min(sms, kShareCtas), run = static_cast<int>((units * tiles + ctas - 1) / ctas);
+    if (run + 12.0 * ((run + tiles - 2) / tiles + 1) + 10.0 + 2.0 * tiles / run < best) {
+      a.S = 1;
+      a.part.per = run;
+      a.part.pages = tiles;
+      a.part.rows = a.rows;
+      a.part.q_tiles = a.q_tiles;
+      int n;
+      return wide_capacity(kind_of(a), 1, sms, &n);   // (readies the kernel)
+    }
+  }
   return cudaSuccess;
 }
 
 cudaError_t launch_attention_wide(cudaStream_t st, const CUtensorMap* tmKV, const AttnWideArgs& a, int batch, bool pdl) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.S, a.Hkv, batch * a.q_tiles);
-  cfg.blockDim = dim3(threads_of(a.share));
-  cfg.dynamicSmemBytes = bytes_of(a.share);
+  const unsigned pages = static_cast<unsigned>(a.Hkv * a.q_tiles) * a.part.pages;
+  cfg.gridDim = a.share == kPrefixPass && a.part.per ? dim3((pages + a.part.per - 1) / a.part.per)
+                                       : dim3(a.S, a.Hkv, batch * a.q_tiles);
+  cfg.blockDim = dim3(threads_of(kind_of(a)));
+  cfg.dynamicSmemBytes = bytes_of(kind_of(a));
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -838,7 +950,7 @@ cudaError_t launch_attention_wide(cudaStream_t st, const CUtensorMap* tmKV, cons
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, wide_kernel(a.share), *tmKV, a);
+  return cudaLaunchKernelEx(&cfg, wide_kernel(kind_of(a)), *tmKV, a);
 }
 
 }  // namespace nld

@@ -2342,9 +2342,15 @@ nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float*
   return NLD_OK;
 }
 
+// Rows of the prefix's partials: a query tile (the last of a kv head's may be short) takes 128, and each CTA's first part of
+// a tile as many again.
+static size_t share_rows(int batch, int m, int n_q_heads) {
+  return static_cast<size_t>(batch) * m * n_q_heads + 128 * (static_cast<size_t>(n_q_heads) + kShareCtas);
+}
+
 size_t nld_attention_shared_workspace_size(int batch, int m, int n_q_heads) {
   if (batch < 1 || m < 1 || n_q_heads < 1) return 0;
-  return static_cast<size_t>(batch) * m * n_q_heads * (128 + 2) * sizeof(float);
+  return share_rows(batch, m, n_q_heads) * (128 + 2) * sizeof(float);
 }
 
 nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const int32_t* d_shared_pages,
@@ -2363,11 +2369,10 @@ nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const in
   const int sms = device_sms();
   const int G = n_q_heads / n_kv_heads;
   const float scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
-  float* part_o = nullptr;   // rows of 512 bytes, then the (max, sum) pairs
-  float2* part_ml = nullptr;
-  if (shared_len > 0) {
-    part_o = static_cast<float*>(d_workspace);
-    part_ml = reinterpret_cast<float2*>(part_o + static_cast<size_t>(batch) * m * n_q_heads * 128);
+  ShareParts part{};
+  if (shared_len > 0) {   // rows of 512 bytes, then the (max, sum) pairs
+    part.o = static_cast<float*>(d_workspace);
+    part.ml = reinterpret_cast<float2*>(part.o + share_rows(batch, m, n_q_heads) * 128);
   }
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   CUtensorMap map;
@@ -2390,8 +2395,7 @@ nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const in
       a.scale_log2 = scale_log2;
       a.share = share;
       a.key_end = shared_len;
-      a.part_o = part_o;
-      a.part_ml = part_ml;
+      a.part = part;
       a.err = d_err;
     };
     cudaError_t e = cudaSuccess;
@@ -2409,6 +2413,7 @@ nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const in
         return fail(nullptr, NLD_ERR_CUDA, "tensor map encode failed (pool)");
       have_map = true;
       e = attn_wide_plan(seqs, max_keys, sms, a);
+      if (share == kPrefixPass) part = a.part;   // where the own pass finds them
       if (e == cudaSuccess && launch) e = launch_attention_wide(st, &map, a, seqs, pdl);
     }
     if (e != cudaSuccess) return fail(nullptr, NLD_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));

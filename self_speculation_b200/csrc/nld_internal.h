@@ -192,6 +192,16 @@ constexpr int kOwnPass = 1, kPrefixPass = 2;
 
 // Attention for small query tiles: over the e4m3 cache (nld_attention_q8), or a pass of the
 // shared-prefix attention over the bf16 cache.
+// Where the prefix pass leaves its rows' unnormalised (O, max, sum), and where the own pass finds them.  per == 0: a row's
+// place is token x Hq + head.  Otherwise the pass was cut into CTAs of `per` pages along all of its (kv head, query tile,
+// page), so that CTA c's part of tile u is 128 rows at place u + c (either grows with every part).
+struct ShareParts {
+  float* o;                     // [place][128] (null: no prefix)
+  float2* ml;                   // [place] running max (log2 units) and sum
+  int per, pages, rows, q_tiles;   // pages of the prefix; rows of a query tile, query tiles of a kv head
+};
+constexpr int kShareCtas = 160; // CTAs of such a pass at most
+
 struct AttnSmallArgs {
   const void* q;                // [batch, m, Hq, 128] bf16
   void* out;
@@ -205,8 +215,7 @@ struct AttnSmallArgs {
   float scale_log2;             // log2(e) / sqrt(hd)
   int share;                    // 0: e4m3; kOwnPass or kPrefixPass: bf16
   int key_end;                  // prefix pass: keys of the prefix
-  float* part_o;                // [tokens x Hq][128] unnormalised prefix O (own pass: null = no prefix)
-  float2* part_ml;              // [tokens x Hq] its running max (log2 units) and sum
+  ShareParts part;
   int* err;
 };
 
@@ -223,8 +232,7 @@ struct AttnWideArgs {
   int q_tiles, rows, S;         // query tiles of a sequence, rows of one, KV splits (cluster size)
   float scale_log2;
   int share, key_end;
-  float* part_o;
-  float2* part_ml;
+  ShareParts part;
   int* err;
 };
 

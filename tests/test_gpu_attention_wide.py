@@ -29,6 +29,18 @@ def test_shared_rows(prefix, lens, m, bs, hq, hkv):
     shared.check(s, shared.run(s, bs), bs)
 
 
+# a prefix pass of more query tiles than SMs: CTAs take runs of pages across them, and the own pass (wide, then
+# small tiles) adds two or three parts of a row
+@pytest.mark.parametrize("prefix,lens,m,bs,hq,hkv,seqs", [
+    (4133, [20] * 16, 32, 32, 40, 8, [0, 3, 4, 15]), (3190, [20] * 30, 16, 16, 40, 40, [0, 7, 8, 29]),
+    (3137, [0, 70, 5, 64, 0, 1, 2, 3, 4, 9], 33, 1, 53, 53, [0, 4, 9])])
+def test_shared_runs_of_pages(prefix, lens, m, bs, hq, hkv, seqs):
+    s = shared.make(prefix, lens, m, hq, hkv, seed=prefix)
+    out = shared.run(s, bs)
+    shared.check(s, out, bs, seqs=seqs)
+    assert torch.equal(out, shared.run(s, bs))
+
+
 def climb(pool, pages, n, raw):
     """Keys whose scores climb page by page (by far more than 2^8 altogether), then fall."""
     j = torch.arange(n)

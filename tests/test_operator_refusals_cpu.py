@@ -58,7 +58,7 @@ def test_attention_shared(bad, want):
 
 
 def test_attention_shared_workspace_size():
-    assert nb.nld_attention_shared_workspace_size(4, 33, 32) == 4 * 33 * 32 * 130 * 4
+    assert nb.nld_attention_shared_workspace_size(4, 33, 32) == (4 * 33 * 32 + 128 * (32 + 160)) * 130 * 4
     assert nb.nld_attention_shared_workspace_size(0, 1, 32) == 0
     assert nb.nld_attention_shared_workspace_size(1, -1, 32) == 0
 
