@@ -1,7 +1,8 @@
 """Python binding of the nld C ABI (include/nld.h): argument marshalling only.
 
 Every step of the decode path runs in the CUDA library `libnld.so` built from `csrc/`.  The
-binding passes raw device pointers of torch tensors; there is no fallback: if the library is
+binding passes raw device pointers of torch tensors (the four operators of a decode step through the C++
+module `_operators.so`); there is no fallback: if the library is
 missing or no GPU is present, the calls raise.
 """
 from __future__ import annotations
