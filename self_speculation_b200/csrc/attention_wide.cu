@@ -39,6 +39,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <atomic>
 #include <mutex>
 
@@ -399,6 +400,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       float down = copysignf(__uint_as_float(static_cast<uint32_t>(134 - e) << 23), ks);   // (the scores' scale stays positive)
       if (big == INFINITY) down = NAN;   // (e4m3 has no infinity)
       c = fabsf(ks) * a.scale_log2 * __uint_as_float(static_cast<uint32_t>(120 + e) << 23);
+      if (c < FLT_MIN) c = FLT_MIN;   // (0 times a masked score would be NaN)
       uint32_t hi[16], lo[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {

@@ -64,6 +64,16 @@ def test_moving_maximum(m):
     shared.check(s, shared.run(s, m), m)
 
 
+@pytest.mark.parametrize("m", [1, 20])
+@pytest.mark.parametrize("zero", ["keys", "queries"])
+def test_scores_that_underflow_weigh_all_keys_alike(m, zero):
+    """A scale of zero (a head whose keys are all zero), a query of zeros with a tiny scale."""
+    s = q8.make([75], m, 8, 2, seed=40 + m, kscale=1e-9 if zero == "queries" else 0.0)
+    if zero == "queries":
+        s["q"].zero_()
+    q8.check(s, q8.run(s, 1), 1)
+
+
 @pytest.mark.parametrize("m", [1, 32])
 def test_negative_scales(m):
     s = q8.make([200], m, 8, 2, seed=20 + m)
