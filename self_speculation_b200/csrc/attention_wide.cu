@@ -21,7 +21,8 @@
 // maximum 175, exponentials 512 to 800, waits 370, P out 100).  Two threads a row (sixteen softmax warps) took 10 to
 // 17 % longer, a quarter of the exponentials as polynomials on the multiply-add pipe 1 to 6 %, the next page's scores
 // fetched under this one's exponentials 9 %, the maximum taken beside the exponentials of a stale one the same time.
-// A CTA's fixed cost is 8 us (Q 2, partials 1, merge 3.5), which few pages a CTA do not hide.
+// A CTA's fixed cost is 8 us (Q 2, partials 1, merge 3.5), which few pages a CTA do not hide; without splits or a prefix the
+// rows go out from the threads that add the streams (64 sequences x 32 rows over 332 keys 62 -> 49 us).
 //
 // A prefix pass may have more query tiles than SMs, and then a round of clusters that few of them fill.  Where it costs less,
 // it is cut into runs of pages (kRuns): a CTA an SM takes as many pages as any other, across query tiles.  Each tile's part
@@ -684,7 +685,8 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     sX[tid] = have ? make_float2(m_ref, l_sum) : make_float2(-INFINITY, 0.f);
   }
   __syncthreads();
-  // a thread adds dims 64 x .. of both streams' rows r
+  // a thread adds dims 64 x .. of both streams' rows r; they are done, then, if there is nothing else to add
+  const bool direct = kShare == 0 && a.S == 1;
   if (softmax_thr) {
     const float2 ml0 = sX[r], ml1 = sX[128 + r];
     const float M = fmaxf(ml0.x, ml1.x);
@@ -692,6 +694,16 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     // (a stream without a tile has no O)
     const bool take0 = __any_sync(0xffffffffu, w0 != 0.f), take1 = __any_sync(0xffffffffu, w1 != 0.f);
     const uint32_t lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * 64;
+    const float L = w0 * ml0.y + w1 * ml1.y;
+    uint4* out = nullptr;
+    float inv = 0.f;
+    if (direct && r < rows) {
+      const int row = r0 + r, pos = row / a.G;
+      out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
+                                     ((static_cast<size_t>(b) * a.m + pos) * a.Hq + static_cast<size_t>(g) * a.G + (row - pos * a.G)) * 128) +
+            8 * x;
+      inv = L > 0.f ? (kQ8 ? a.v_scale[g] : 1.f) / L : 0.f;
+    }
 #pragma unroll 1
     for (int u = 0; u < 2; ++u) {
       uint32_t o0[32], o1[32];
@@ -710,10 +722,18 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
         if (w1 != 0.f)
           v = make_float4(fmaf(__uint_as_float(o1[k]), w1, v.x), fmaf(__uint_as_float(o1[k + 1]), w1, v.y),
                           fmaf(__uint_as_float(o1[k + 2]), w1, v.z), fmaf(__uint_as_float(o1[k + 3]), w1, v.w));
-        *reinterpret_cast<float4*>(sO + r * 128 + (((x * 16 + u * 8 + (k >> 2)) ^ (r & 31)) << 2)) = v;
+        if (!direct) {
+          *reinterpret_cast<float4*>(sO + r * 128 + (((x * 16 + u * 8 + (k >> 2)) ^ (r & 31)) << 2)) = v;
+        } else {
+          o0[k >> 1] = pack16<false>(v.x * inv, v.y * inv);
+          o0[(k >> 1) + 1] = pack16<false>(v.z * inv, v.w * inv);
+        }
       }
+      if (direct && out != nullptr)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[4 * u + k] = make_uint4(o0[4 * k], o0[4 * k + 1], o0[4 * k + 2], o0[4 * k + 3]);
     }
-    if (x == 0) sML[r] = make_float2(M, w0 * ml0.y + w1 * ml1.y);
+    if (x == 0) sML[r] = make_float2(M, L);
     if constexpr (runs) fence_proxy_async();
     if constexpr (kShare == kOwnPass && kRuns)
       if (x == 1 && r < rows) {
@@ -729,6 +749,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (direct) break;
 
   if constexpr (runs) {   // a part is left as it lies here, by a copy that only the next part's loads wait for
     if (load_thr) {
@@ -906,13 +927,13 @@ cudaError_t attn_wide_plan(int batch, int max_len, int sms, AttnWideArgs& a) {
   a.rows = (all + a.q_tiles - 1) / a.q_tiles;
   const long long units = static_cast<long long>(batch) * a.q_tiles * a.Hkv;
   const int tiles = (max_len + kTile - 1) / kTile;
-  // The fewest rounds of resident clusters times a round's length, a tile 1 and the rest of a CTA 16
+  // The fewest rounds of resident clusters times a round's length, a tile 1 and the rest of a CTA 16, without a merge 11
   double best = 0;
   for (int S = 1; S <= 8 && S <= tiles; ++S) {
     int cap = 1;
     const cudaError_t e = wide_capacity(kind_of(a), S, sms, &cap);
     if (e != cudaSuccess) return e;
-    const double cost = static_cast<double>((units + cap - 1) / cap) * ((tiles + S - 1) / S + 16.0);
+    const double cost = static_cast<double>((units + cap - 1) / cap) * ((tiles + S - 1) / S + (S == 1 && !a.share ? 11.0 : 16.0));
     if (S == 1 || cost < best) {
       best = cost;
       a.S = S;
