@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
                                      ((static_cast<size_t>(b) * a.m + pos) * a.Hq + static_cast<size_t>(g) * a.G + (row - pos * a.G)) * 128) +
             8 * x;
-      inv = L > 0.f ? (kQ8 ? a.v_scale[g] : 1.f) / L : 0.f;
+      inv = (kQ8 ? a.v_scale[g] : 1.f) / L;   // (a row sees its own key at least; NaN comes out)
     }
 #pragma unroll 1
     for (int u = 0; u < 2; ++u) {
@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       }
       if constexpr (kShare == kOwnPass)
         if (!kRuns && a.part.o != nullptr) share_add(pre_ml[i], pre[i], M[i], L[i], acc[i]);
-      const float k = L[i] > 0.f ? vscale / L[i] : 0.f;
+      const float k = vscale / L[i];   // (a row sees its own key at least; NaN comes out)
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at[i] * 128 + 4 * d4) =
           make_uint2(pack16<false>(acc[i].x * k, acc[i].y * k), pack16<false>(acc[i].z * k, acc[i].w * k));
     }

@@ -1,0 +1,117 @@
+"""NaN and infinities in nld_attention_q8 and nld_attention_shared: what the
+definition makes of them, alike for small and wide query tiles, with and without splits of the keys.
+
+Rows are worked on apart, so a row without such a number has the bits of the same call without any."""
+import pytest
+import torch
+
+import test_gpu_attention_q8 as q8
+import test_gpu_attention_shared as shared
+
+pytestmark = pytest.mark.gpu
+
+HQ, HKV = 8, 4
+
+# keys of one sequence: a page, several streams, splits; 1 row (small tiles) and 40 rows (wide ones)
+SHAPES = [(m, n) for m in (1, 40) for n in (0, 64, 128, 900)]
+# (prefix, own keys): one page of either; splits of the prefix; none
+SHARED_SHAPES = [(m, p, n) for m in (1, 40) for p, n in ((1, 0), (65, 64), (512, 300), (2200, 5), (0, 130))]
+RUNS = (33, 3137, 20, 10)   # rows, prefix, own keys, sequences: a prefix pass in runs of pages (HKV = HQ = 53)
+
+
+def q8_at(m, n):
+    return q8.make([n], m, HQ, HKV, seed=m + n)
+
+
+def shared_at(m, p, n):
+    return shared.make(p, [n], m, HQ, HKV, seed=m + p + n)
+
+
+def poison_keys(s, pages, first, end, head):
+    """NaN in the K rows first..end-1 of a list of pages."""
+    j = torch.arange(first, end)
+    if s["pool"].dtype == torch.bfloat16:
+        s["pool"][pages[j // 64].long(), 0, head, j % 64, 5] = float("nan")
+    else:
+        s["pool"].view(torch.uint8)[pages[j // 64].long(), 0, head, j % 64, 5] = 0xff
+
+
+def only_rows_are_nan(out, clean, bad):
+    """bad: truth value of each (sequence, row, head)."""
+    out, clean = out.float(), clean.float()
+    assert out[bad].isnan().all(), out[bad]
+    assert torch.equal(out[~bad], clean[~bad])
+
+
+def poison_query(s, value, at):
+    s["q"][at][3] = value
+    bad = torch.zeros(s["q"].shape[:3], dtype=torch.bool)
+    bad[at] = True
+    return bad
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("m,n", SHAPES)
+def test_q8_query(m, n, value):
+    s = q8_at(m, n)
+    clean = q8.run(s, m)
+    bad = poison_query(s, value, (0, m // 2, 5))
+    only_rows_are_nan(q8.run(s, m), clean, bad)
+
+
+@pytest.mark.parametrize("m,p,n", SHARED_SHAPES)
+def test_shared_query(m, p, n):
+    s = shared_at(m, p, n)
+    clean = shared.run(s, m)
+    bad = poison_query(s, float("nan"), (0, m // 2, 5))
+    only_rows_are_nan(shared.run(s, m), clean, bad)
+
+
+def test_shared_query_with_infinities():
+    """Every key's score is -inf: 0 / 0."""
+    for m in (1, 40):
+        s = shared_at(m, 512, 300)
+        s["pool"][..., 3] = s["pool"][..., 3].abs() + 1     # (NaN slots stay)
+        clean = shared.run(s, m)
+        bad = poison_query(s, float("-inf"), (0, m // 2, 5))
+        only_rows_are_nan(shared.run(s, m), clean, bad)
+
+
+def head_rows(s, head):
+    bad = torch.zeros(s["q"].shape[:3], dtype=torch.bool)
+    bad[:, :, head * HQ // HKV:(head + 1) * HQ // HKV] = True
+    return bad
+
+
+@pytest.mark.parametrize("m,n", SHAPES)
+def test_q8_first_new_key(m, n):
+    """At a page's start it is the only key of a stream, or of a key group, that the first row sees."""
+    s = q8_at(m, n)
+    clean = q8.run(s, 1)
+    poison_keys(s, s["table"][0], n, n + 1, 2)
+    only_rows_are_nan(q8.run(s, 1), clean, head_rows(s, 2))
+
+
+@pytest.mark.parametrize("m,p,n", [a for a in SHARED_SHAPES if a[1]])
+@pytest.mark.parametrize("where", ["last key of the prefix", "first new key"])
+def test_shared_keys(m, p, n, where):
+    s = shared_at(m, p, n)
+    clean = shared.run(s, 1)
+    if where == "first new key":
+        poison_keys(s, s["table"][0], n, n + 1, 2)
+    else:
+        poison_keys(s, s["sp"], p - 1, p, 2)
+    only_rows_are_nan(shared.run(s, 1), clean, head_rows(s, 2))
+
+
+def test_shared_runs_of_pages():
+    m, p, n, batch = RUNS
+    s = shared.make(p, [n] * batch, m, 53, 53, seed=1)
+    clean = shared.run(s, 1)
+    bad = poison_query(s, float("nan"), (batch - 1, 7, 50))
+    only_rows_are_nan(shared.run(s, 1), clean, bad)
+    s = shared.make(p, [n] * batch, m, 53, 53, seed=1)
+    poison_keys(s, s["sp"], 64, p, 20)
+    bad = torch.zeros(batch, m, 53, dtype=torch.bool)
+    bad[:, :, 20] = True
+    only_rows_are_nan(shared.run(s, 1), clean, bad)
