@@ -502,15 +502,17 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
     float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (ml[q].x != -INFINITY) {
-        const float w = exp2f(ml[q].x - M);
-        L += w * ml[q].y;
+    for (int q = 0; q < 8; ++q) {
+      const bool none = ml[q].x == -INFINITY;
+      const float w = none ? 0.f : exp2f(ml[q].x - M);
+      L += w * ml[q].y;   // (a split that has met only NaN: no maximum, a sum of NaN)
+      if (!none) {
         acc.x += w * ov[q].x;
         acc.y += w * ov[q].y;
         acc.z += w * ov[q].z;
         acc.w += w * ov[q].w;
       }
+    }
     store_row(r, acc, M, L);
   }
   cluster_sync();   // peers may still be reading this CTA's shared memory

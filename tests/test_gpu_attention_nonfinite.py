@@ -92,15 +92,25 @@ def test_q8_first_new_key(m, n):
     only_rows_are_nan(q8.run(s, 1), clean, head_rows(s, 2))
 
 
+@pytest.mark.parametrize("m,max_len", [(1, 512), (16, 512), (40, 512), (40, 64 * 9)])
+def test_q8_keys_of_a_split(m, max_len):
+    """Of 3 pages the last, with a split of its own."""
+    s = q8_at(m, 128)
+    s["table"] = torch.cat((s["table"], s["table"].new_zeros(1, 8)), 1).contiguous()
+    clean = q8.run(s, 1, max_len=max_len)
+    poison_keys(s, s["table"][0], 128, 128 + m, 1)
+    only_rows_are_nan(q8.run(s, 1, max_len=max_len), clean, head_rows(s, 1))
+
+
 @pytest.mark.parametrize("m,p,n", [a for a in SHARED_SHAPES if a[1]])
-@pytest.mark.parametrize("where", ["last key of the prefix", "first new key"])
+@pytest.mark.parametrize("where", ["last key of the prefix", "last half of the prefix", "first new key"])
 def test_shared_keys(m, p, n, where):
     s = shared_at(m, p, n)
     clean = shared.run(s, 1)
     if where == "first new key":
         poison_keys(s, s["table"][0], n, n + 1, 2)
     else:
-        poison_keys(s, s["sp"], p - 1, p, 2)
+        poison_keys(s, s["sp"], p - 1 if where[5] == "k" else (p + 63) // 128 * 64, p, 2)
     only_rows_are_nan(shared.run(s, 1), clean, head_rows(s, 2))
 
 
