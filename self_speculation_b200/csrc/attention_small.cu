@@ -503,14 +503,15 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const bool none = ml[q].x == -INFINITY;
-      const float w = none ? 0.f : exp2f(ml[q].x - M);
-      L += w * ml[q].y;   // (a split that has met only NaN: no maximum, a sum of NaN)
-      if (!none) {
+      if (ml[q].x != -INFINITY) {
+        const float w = exp2f(ml[q].x - M);
+        L += w * ml[q].y;
         acc.x += w * ov[q].x;
         acc.y += w * ov[q].y;
         acc.z += w * ov[q].z;
         acc.w += w * ov[q].w;
+      } else {
+        L += 0.f * ml[q].y;   // (a split that has met only NaN: no maximum, a sum of NaN)
       }
     }
     store_row(r, acc, M, L);
