@@ -491,8 +491,8 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
  *                outside the pool reads as zeros, and NLD_DEVERR_KV_OVERFLOW is or-ed in;
  *                NLD_DEVERR_TIMEOUT if a bounded wait ran out.
  * The other arguments, the mask and the conventions are those of nld_attention (d_q and d_out
- * bf16, 16-byte aligned).  Scores, maxima and sums are fp32; the probabilities are rounded to fp16 for
- * their product with V.  Elements of a query row below 2^-9 of its largest may be off by 2^-17 of that
+ * bf16, 16-byte aligned).  Scores, maxima and sums are fp32; the probabilities are rounded to fp16's 11 bits for
+ * their product with V (below 2^-25 of the row's largest to steps of 2^-35 of it).  Elements of a query row below 2^-9 of its largest may be off by 2^-17 of that
  * one in its products with K (below 2^-14 of it by 2^-25, for the small tiles).
  */
 nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float* d_k_scale, const float* d_v_scale,

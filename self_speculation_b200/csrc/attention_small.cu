@@ -18,8 +18,10 @@
 // e4m3 is exact in fp16, so its products run in fp16 with fp32 accumulators: Q's rows are scaled by
 // a power of two into fp16's range (bf16's 8 significant bits fit its 11; what falls below 2^-24 of
 // the row's largest element rounds at that size, far under fp32's own error of the sum), P is
-// rounded to fp16 (half a step 2^-12 of it, an eighth of the output's own bf16 rounding).  Over the bf16
-// cache Q goes in as it is and P is rounded to bf16, as in attention.cu.  Maxima, sums and O stay
+// rounded to fp16: half a step is 2^-11 of it, an eighth of the output's own bf16 rounding.  P is 2^15 at the row's
+// maximum (the division by the sum takes that out), so it keeps all its bits down to 2^-29 of the largest and is off
+// by 2^-40 of that at most below; with 1 there it would be 2^-14 and 2^-25, which many keys of a long cache add up.
+// Over the bf16 cache Q goes in as it is and P is rounded to bf16, as in attention.cu.  Maxima, sums and O stay
 // in fp32.  Both scales are applied to fp32 values: k_scale within the score's scale, v_scale at the end.
 //
 // 64 sequences of 1024..8192 keys, 32 / 8 heads, one row each: 124 us for 622 MB (5.0 TB/s); copies laid out by
@@ -45,6 +47,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStages = 2;         // steps of a warp in flight
 constexpr int kStepBytes = 8192;   // of K, then of V, half each
+constexpr float kShift = 15.f;     // e4m3: log2 of P at the maximum
 constexpr int kRowFloats = 132;    // a partial row in shared memory: 128 dims, max, sum
 constexpr int kRing = kWarps * kStages * kStepBytes;   // 64 KB; the partials overlay it
 static_assert(kRing >= kWarps * 16 * kRowFloats * 4, "partials");
@@ -322,6 +325,10 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
       mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 2));
       mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 1));
       mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 2));
+      if constexpr (kQ8) {   // the reference, rounded up: P does not exceed 2^kShift
+        mx_a = __fadd_ru(mx_a, -kShift);
+        mx_b = __fadd_ru(mx_b, -kShift);
+      }
       if (__any_sync(0xffffffffu, mx_a > m_a || mx_b > m_b)) {
         const float n_a = fmaxf(m_a, mx_a), n_b = fmaxf(m_b, mx_b);
         // (the first finite maximum of a row scales zeros)
@@ -444,8 +451,8 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
         else share_add(a.part.ml[at], reinterpret_cast<const float4*>(a.part.o)[at * 32 + lane], M, L, v);
       }
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at * 128;
-    const float k = vs / L;   // a row sees its own key at least
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * k, v.y * k), hi = __floats2bfloat162_rn(v.z * k, v.w * k);
+    const float k = 1.f / L;   // a row sees its own key at least
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * k * vs, v.y * k * vs), hi = __floats2bfloat162_rn(v.z * k * vs, v.w * k * vs);
     *reinterpret_cast<uint2*>(dst + 4 * lane) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   };

@@ -32,10 +32,12 @@
 //
 // bf16: K and V come by TMA into rings of six pages.  e4m3: K's page goes to the tensor core as it comes (kind::f8f6f4)
 // against Q in two e4m3 parts (split_e4m3); V's comes by bulk copies, and four warps turn it into an fp16 tile (exact)
-// in the swizzled layout of the descriptors, for P rounded to fp16 (attention_small.cu has that error).  Converting K
+// in the swizzled layout of the descriptors, for P rounded to fp16: 2^11 to 2^15 at the row's maximum, so it has fp16's 11
+// bits down to 2^-25 of the largest and is off by 2^-36 of that at most below (as in attention_small.cu).  Converting K
 // as well took 95 us with eight warps and 166 with four; by integer operations instead of the cvt, 141 with eight.
 // K's place frees when S is done, V's when O is.  Over the bf16 cache P is rounded to bf16.  The maximum that exponents
-// refer to moves only when it has grown by 2^8, so O is rarely rescaled; sums, maxima and O are in fp32.
+// refer to moves only when it has grown by 2^8 (e4m3: 2^4, that P stays in fp16), so O is rarely rescaled; sums, maxima
+// and O are in fp32.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -56,12 +58,12 @@ constexpr int kTileBytes = kTile * 256;      // K (or V) of a tile in 16 bits: [
 constexpr int kBoxBytes = kTileBytes / 2;
 constexpr int kRawBytes = kTile * 128;       // the same in e4m3: [64 keys][128 B]
 constexpr int kSoftmax = 256;                // threads: two streams of 128, a row each
-constexpr float kMove = 8.f;                 // log2 units
 constexpr uint64_t kWait = 2000000000ull;
 
 template <typename E>
 struct Wide {   // bf16
   static constexpr bool kQ8 = false;
+  static constexpr float kShift = 0.f, kMove = 8.f;     // log2 units: P at a new reference, and how far it may rise
   static constexpr int kK = 6, kV = 6, kRaw = 0;        // tiles of K, of V, raw ones of V
   static constexpr int kKBytes = kTileBytes;
   static constexpr int kThreads = kSoftmax + 96;        // two issuing warps, a loading one
@@ -69,6 +71,7 @@ struct Wide {   // bf16
 template <>
 struct Wide<__nv_fp8_storage_t> {
   static constexpr bool kQ8 = true;
+  static constexpr float kShift = 11.f, kMove = 4.f;
   static constexpr int kK = 6, kV = 4, kRaw = 4;
   static constexpr int kKBytes = kRawBytes;
   static constexpr int kThreads = kSoftmax + 96 + 128;   // and four converting ones
@@ -543,8 +546,9 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int k = 0; k < kTile; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(s[k >> 5][k & 31]));
-      const float mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;
-      const bool move = mx > m_ref + kMove;
+      float mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;
+      if constexpr (kQ8) mx = __fadd_ru(mx, -W::kShift);
+      const bool move = mx > m_ref + W::kMove;
       const bool scale_o = move && m_ref != -INFINITY;
       if (__any_sync(0xffffffffu, scale_o)) {   // (i > 0: m_ref was set)
         if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(first + i - 1) & 1u, kWait))) {
@@ -696,13 +700,14 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     const uint32_t lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * 64;
     const float L = w0 * ml0.y + w1 * ml1.y;
     uint4* out = nullptr;
-    float inv = 0.f;
+    float inv = 0.f, vscale = 1.f;
+    if constexpr (kQ8) vscale = a.v_scale[g];
     if (direct && r < rows) {
       const int row = r0 + r, pos = row / a.G;
       out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
                                      ((static_cast<size_t>(b) * a.m + pos) * a.Hq + static_cast<size_t>(g) * a.G + (row - pos * a.G)) * 128) +
             8 * x;
-      inv = (kQ8 ? a.v_scale[g] : 1.f) / L;   // (a row sees its own key at least; NaN comes out)
+      inv = 1.f / L;   // (a row sees its own key at least; NaN comes out)
     }
 #pragma unroll 1
     for (int u = 0; u < 2; ++u) {
@@ -725,8 +730,8 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
         if (!direct) {
           *reinterpret_cast<float4*>(sO + r * 128 + (((x * 16 + u * 8 + (k >> 2)) ^ (r & 31)) << 2)) = v;
         } else {
-          o0[k >> 1] = pack16<false>(v.x * inv, v.y * inv);
-          o0[(k >> 1) + 1] = pack16<false>(v.z * inv, v.w * inv);
+          o0[k >> 1] = pack16<false>(v.x * inv * vscale, v.y * inv * vscale);
+          o0[(k >> 1) + 1] = pack16<false>(v.z * inv * vscale, v.w * inv * vscale);
         }
       }
       if (direct && out != nullptr)
@@ -860,9 +865,9 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       }
       if constexpr (kShare == kOwnPass)
         if (!kRuns && a.part.o != nullptr) share_add(pre_ml[i], pre[i], M[i], L[i], acc[i]);
-      const float k = vscale / L[i];   // (a row sees its own key at least; NaN comes out)
+      const float k = 1.f / L[i];   // (a row sees its own key at least; NaN comes out)
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at[i] * 128 + 4 * d4) =
-          make_uint2(pack16<false>(acc[i].x * k, acc[i].y * k), pack16<false>(acc[i].z * k, acc[i].w * k));
+          make_uint2(pack16<false>(acc[i].x * k * vscale, acc[i].y * k * vscale), pack16<false>(acc[i].z * k * vscale, acc[i].w * k * vscale));
     }
   }
   break;

@@ -1,4 +1,4 @@
-"""NaN and infinities in nld_attention_q8 and nld_attention_shared: what the
+"""NaN, infinities and weights far under the largest in nld_attention_q8 and nld_attention_shared: what the
 definition makes of them, alike for small and wide query tiles, with and without splits of the keys.
 
 Rows are worked on apart, so a row without such a number has the bits of the same call without any."""
@@ -125,3 +125,32 @@ def test_shared_runs_of_pages():
     bad = torch.zeros(batch, m, 53, dtype=torch.bool)
     bad[:, :, 20] = True
     only_rows_are_nan(shared.run(s, 1), clean, bad)
+
+
+@pytest.mark.parametrize("m", [1, 16, 40])
+@pytest.mark.parametrize("nats", [8.0, 17.0, 20.0])
+def test_q8_many_keys_of_little_weight(m, nats):
+    """The row's likeliest key has a V of zeros, n others e^-nats of its weight and a V of ones: o = n e^-nats /
+    (1 + n e^-nats) comes from weights that fp16 alone holds badly (17 nats are 2^-24.5).
+
+    The probabilities go in as fp16 of 2^15 p or less, 2^11 p at least for the likeliest key: off by 2^-11 of each, and
+    by 2^-36 of the likeliest's each: 2^-11 o + n 2^-36; the scores by d = 136 2^-24 A (A the largest sum |q k| scale), and
+    ex2's 2^-22 beside it, which moves o by 2 (d + 2^-22) o; sums in fp32 n 2^-23 o; the output 2^-8 o."""
+    n = 3000
+    s = q8.make([n], m, HQ, HKV, seed=m)
+    j = torch.arange(n + m)
+    rows = torch.zeros(n + m, 2, HKV, 128)
+    rows[:, 1] = 1.0
+    rows[100, 0, :, 7] = 8.0
+    rows[100, 1] = 0.0
+    s["pool"].view(torch.uint8)[s["table"][0, j // 64].long(), :, :, j % 64] = rows.to(torch.float8_e4m3fn).view(torch.uint8)
+    s["ks"], s["vs"] = torch.ones(HKV), torch.full((HKV,), 3.0)
+    s["q"].zero_()
+    s["q"][..., 7] = nats * 128 ** 0.5 / 8
+    score = float(s["q"][0, 0, 0, 7].double()) * 8 * 128 ** -0.5      # of the likeliest key, the others' being 0
+    others = (n + torch.arange(m)).double()                         # that row i sees
+    little = others * torch.exp(torch.tensor(-score, dtype=torch.float64))
+    want = 3 * (little / (1 + little))[:, None, None]
+    tol = want * (2.0 ** -8 + 2.0 ** -11 + 2 * (136 * 2.0 ** -24 * score + 2.0 ** -22) + n * 2.0 ** -23) + 3 * n * 2.0 ** -36
+    got = q8.run(s, 1)[0].double()
+    assert ((got - want).abs() <= tol).all(), (got[0, 0, 0], want[0], tol[0])
