@@ -58,6 +58,7 @@ constexpr int kTileBytes = kTile * 256;      // K (or V) of a tile in 16 bits: [
 constexpr int kBoxBytes = kTileBytes / 2;
 constexpr int kRawBytes = kTile * 128;       // the same in e4m3: [64 keys][128 B]
 constexpr int kSoftmax = 256;                // threads: two streams of 128, a row each
+constexpr float kFar = 1048576.f;            // log2 units: from here on a step is 1/8 and more
 constexpr uint64_t kWait = 2000000000ull;
 
 template <typename E>
@@ -518,7 +519,6 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
     const int seen = r < rows ? seen_by(r0 + r) : 0;
     const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lane + s_col_of(x), p_at = tmem + lane + p_col_of(x), o_at = tmem + lane + o_col_of(x);
-    const f2 c2 = pair(c, c);
     const int mine = ntile > x ? (ntile - x + 1) / 2 : 0;   // tiles of the stream
     const int first = x ? done_1 : done_0;
     for (int i = 0; i < mine; ++i) {
@@ -547,10 +547,13 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
 #pragma unroll
       for (int k = 0; k < kTile; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(s[k >> 5][k & 31]));
       float mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;
+      const bool far = fabsf(mx) > kFar && fabsf(mx) < INFINITY;
+      // (rounded so that the largest exponent is kShift + kMove at most)
       if constexpr (kQ8) mx = __fadd_ru(mx, -W::kShift);
-      const bool move = mx > m_ref + W::kMove;
+      const bool move = mx > __fadd_rd(m_ref, W::kMove);
       const bool scale_o = move && m_ref != -INFINITY;
-      if (__any_sync(0xffffffffu, scale_o)) {   // (i > 0: m_ref was set)
+      const bool rare = __any_sync(0xffffffffu, scale_o || far);
+      if (rare && __any_sync(0xffffffffu, scale_o)) {   // (i > 0: m_ref was set)
         if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], static_cast<uint32_t>(first + i - 1) & 1u, kWait))) {
           aborted = true;
           break;
@@ -571,20 +574,37 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
       }
       if (move) m_ref = mx;
       const float nb = m_ref == -INFINITY ? 0.f : -m_ref;
-      const f2 nb2 = pair(nb, nb);
+      const f2 c2 = pair(c, c), nb2 = pair(nb, nb);
       f2 ls[2] = {0, 0};
       uint32_t p[2][16];
+      if (rare && __any_sync(0xffffffffu, far)) {
+        // As below, but scores rounded before the reference is taken off: kept unrounded by the multiply-add, the largest one
+        // could lie half a step of fp32 from its rounded self, and its exponential be 0 or infinite.  (Apart from the usual
+        // code, whose registers it would move: a branch that changes the scores costs 3 %, this 1 % of a bf16 pass at most.)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const f2 e2 = fma2(pair(__uint_as_float(s[h][2 * k]), __uint_as_float(s[h][2 * k + 1])), c2, nb2);
-          float p0, p1;
-          unpair(e2, p0, p1);
-          p0 = exp2_hw(p0);
-          p1 = exp2_hw(p1);
-          ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
-          p[h][k] = pack16<kQ8>(p0, p1);
+          for (int k = 0; k < 16; ++k) {
+            float p0 = __uint_as_float(s[h][2 * k]), p1 = __uint_as_float(s[h][2 * k + 1]);
+            p0 = exp2_hw(__fmul_rn(p0, c) + nb);
+            p1 = exp2_hw(__fmul_rn(p1, c) + nb);
+            ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
+            p[h][k] = pack16<kQ8>(p0, p1);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const f2 e2 = fma2(pair(__uint_as_float(s[h][2 * k]), __uint_as_float(s[h][2 * k + 1])), c2, nb2);
+            float p0, p1;
+            unpair(e2, p0, p1);
+            p0 = exp2_hw(p0);
+            p1 = exp2_hw(p1);
+            ls[k & 1] = add2(ls[k & 1], pair(p0, p1));
+            p[h][k] = pack16<kQ8>(p0, p1);
+          }
         }
       }
       // P is free once O += P V of the tile before has read it

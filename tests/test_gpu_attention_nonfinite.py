@@ -1,4 +1,4 @@
-"""NaN, infinities and weights far under the largest in nld_attention_q8 and nld_attention_shared: what the
+"""NaN, infinities, scores and weights far out of the ordinary in nld_attention_q8 and nld_attention_shared: what the
 definition makes of them, alike for small and wide query tiles, with and without splits of the keys.
 
 Rows are worked on apart, so a row without such a number has the bits of the same call without any."""
@@ -154,3 +154,39 @@ def test_q8_many_keys_of_little_weight(m, nats):
     tol = want * (2.0 ** -8 + 2.0 ** -11 + 2 * (136 * 2.0 ** -24 * score + 2.0 ** -22) + n * 2.0 ** -23) + 3 * n * 2.0 ** -36
     got = q8.run(s, 1)[0].double()
     assert ((got - want).abs() <= tol).all(), (got[0, 0, 0], want[0], tol[0])
+
+
+# scores of 2^(size - 4) and more, where fp32's step comes to be far over 1
+@pytest.mark.parametrize("size", [20, 24, 27, 33, 40, 80])
+@pytest.mark.parametrize("m", [1, 16, 40])
+@pytest.mark.parametrize("at", [0, 70, 899])
+def test_huge_scores_leave_the_likeliest_key(m, size, at):
+    """One key is aligned with the queries, the others' products are lower by a quarter of its own, which is
+    64 2^12 / sqrt(128) nats at least: o is that key's V row, off by the output's rounding 2^-8, that of its P, 2^-11 (bf16:
+    2^-8), and ex2's 2^-22, the fp32 scales' and quotient's 2^-21."""
+    g = torch.Generator().manual_seed(size + at)
+    x = torch.randn(128, generator=g).sign()
+    keys = torch.randn(900 + m, HKV, 128, generator=g).to(torch.float8_e4m3fn).float()
+    keys[at] = 2 * x
+    products = (keys @ x).flatten().topk(HKV + 1).values
+    assert products[HKV - 1] == 256 and products[HKV] < 192
+    up = torch.linspace(1, 1.5, m * HQ).view(1, m, HQ, 1)            # rows of different sizes
+    s = q8.make([900], m, HQ, HKV, seed=1)
+    j = torch.arange(900 + m)
+    page = s["table"][0, j // 64].long()
+    s["pool"].view(torch.uint8)[page, 0, :, j % 64] = keys.to(torch.float8_e4m3fn).view(torch.uint8)
+    s["ks"] = torch.full((HKV,), 2.0 ** (size - 8))
+    s["q"] = (up * x).to(torch.bfloat16)
+    want = s["pool"][page[at], 1, :, at % 64].float() * s["vs"][:, None]
+    want = want.repeat_interleave(HQ // HKV, 0)
+    got = q8.run(s, 1)[0].float()
+    assert ((got - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20)).all(), got[:, :, 0]
+    s = shared.make(700, [200], m, HQ, HKV, seed=1)
+    for pages, first, end in ((s["sp"], 0, 700), (s["table"][0], 700, 900 + m)):
+        j = torch.arange(end - first)
+        s["pool"][pages[j // 64].long(), 0, :, j % 64] = keys[first:end].to(torch.bfloat16)
+    s["q"] = (up * x * 2.0 ** (size - 8)).to(torch.bfloat16)
+    pages, j = (s["sp"], at) if at < 700 else (s["table"][0], at - 700)
+    want = s["pool"][pages[j // 64].long(), 1, :, j % 64].float().repeat_interleave(HQ // HKV, 0)
+    got = shared.run(s, 1)[0].float()
+    assert ((got - want).abs() <= want.abs() * (2 * 2.0 ** -8 + 2.0 ** -20)).all(), got[:, :, 0]
