@@ -209,6 +209,10 @@ NLD_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "mem
 NLD_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }   // the source is free
 NLD_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }             // the copies are done
 
+// Weight of a part of a row whose maximum is m in the sum of parts, M their largest: 0 where the row sees none of its keys
+// (its O may hold anything), else the smallest number at least, so that NaN in a V row that it sees comes out.
+NLD_DEV float merge_weight(float m, float M) { return m == -INFINITY ? 0.f : fmaxf(exp2f(m - M), 1.4e-45f); }
+
 // Columns of tensor memory.
 NLD_DEV constexpr uint32_t s_col_of(int stream) { return stream * 96; }
 NLD_DEV constexpr uint32_t p_col_of(int stream) { return stream * 96 + 64; }
@@ -714,7 +718,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
   if (softmax_thr) {
     const float2 ml0 = sX[r], ml1 = sX[128 + r];
     const float M = fmaxf(ml0.x, ml1.x);
-    const float w0 = ml0.x == -INFINITY ? 0.f : exp2f(ml0.x - M), w1 = ml1.x == -INFINITY ? 0.f : exp2f(ml1.x - M);
+    const float w0 = merge_weight(ml0.x, M), w1 = merge_weight(ml1.x, M);
     // (a stream without a tile has no O)
     const bool take0 = __any_sync(0xffffffffu, w0 != 0.f), take1 = __any_sync(0xffffffffu, w1 != 0.f);
     const uint32_t lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * 64;
@@ -833,7 +837,7 @@ __global__ void __launch_bounds__(Wide<E>::kThreads, 1)
 #pragma unroll
       for (int off = 4; off > 0; off >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], off));
       M[i] = __shfl_sync(0xffffffffu, M[i], 0);
-      w[i] = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - M[i]);
+      w[i] = merge_weight(ml[i].x, M[i]);
       L[i] = w[i] * ml[i].y;
 #pragma unroll
       for (int off = 4; off > 0; off >>= 1) L[i] += __shfl_xor_sync(0xffffffffu, L[i], off);

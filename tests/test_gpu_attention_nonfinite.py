@@ -2,6 +2,8 @@
 definition makes of them, alike for small and wide query tiles, with and without splits of the keys.
 
 Rows are worked on apart, so a row without such a number has the bits of the same call without any."""
+import math
+
 import pytest
 import torch
 
@@ -125,6 +127,45 @@ def test_shared_runs_of_pages():
     bad = torch.zeros(batch, m, 53, dtype=torch.bool)
     bad[:, :, 20] = True
     only_rows_are_nan(shared.run(s, 1), clean, bad)
+
+
+VANISHING = [(100, 70), (100, 5), (900, 70), (900, 470), (900, 700)]   # cached keys, the one whose V is not finite
+
+
+def check_vanishing(out):
+    head = slice(2 * HQ // HKV, 3 * HQ // HKV)
+    assert not torch.isfinite(out[:, head, 5]).any()
+    assert torch.isfinite(out[:, head, 6:]).all() and torch.isfinite(out[:, :head.start]).all()
+
+
+@pytest.mark.parametrize("m", [1, 40])
+@pytest.mark.parametrize("n,at", VANISHING)
+def test_q8_visible_value_of_vanishing_weight(m, n, at):
+    """Key 3's weight is about 2^200 times the others': that of NaN rounds to 0, in the stream, key group or split of
+    key 3 or in another, and 0 times NaN is NaN."""
+    s = q8.make([n], m, HQ, HKV, seed=n)
+    raw = s["pool"].view(torch.uint8)
+    raw[s["table"][0, 0], 0, :, 3, 7] = 0x7e     # 448
+    raw[s["table"][0, at // 64], 1, 2, at % 64, 5] = 0xff
+    s["ks"] = torch.ones(HKV)
+    s["q"].zero_()
+    s["q"][..., 7] = 200 * math.log(2) * 128 ** 0.5 / 448
+    check_vanishing(q8.run(s, 1)[0].float())
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("m", [1, 40])
+@pytest.mark.parametrize("n,at", VANISHING)
+def test_shared_visible_value_of_vanishing_weight(m, n, at, value):
+    """The same; an infinity gives NaN or an infinity."""
+    p = n // 2
+    s = shared.make(p, [n - p], m, HQ, HKV, seed=n)
+    s["pool"][s["sp"][0], 0, :, 3, 7] = 448
+    page = s["sp"][at // 64] if at < p else s["table"][0, (at - p) // 64]
+    s["pool"][page, 1, 2, (at if at < p else at - p) % 64, 5] = value
+    s["q"].zero_()
+    s["q"][..., 7] = 200 * math.log(2) * 128 ** 0.5 / 448
+    check_vanishing(shared.run(s, 1)[0].float())
 
 
 @pytest.mark.parametrize("m", [1, 16, 40])
