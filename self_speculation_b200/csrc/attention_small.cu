@@ -5,9 +5,9 @@
 //   o = softmax(q K^T / sqrt(hd) + mask) V;   e4m3: K = k_scale[g] k8,  V = v_scale[g] v8
 //
 // with the mask of attention.cu.  Bound by HBM: 256 (bf16: 512) bytes per key and kv head, read once per
-// tile of query rows.  One CTA per (KV split, kv head, sequence x tile of 16 kMT query rows), row =
-// position * G + head, so the G heads of a kv head share its K and V.  Its 4 warps are kMT row
-// tiles x 4 / kMT key groups; a warp walks its own pages with an online softmax of its own, kStages
+// query tile.  One CTA per (KV split, kv head, sequence) takes all of the up to 32 query rows, row =
+// position * G + head, so the G heads of a kv head share its K and V.  Its 4 warps are kMT (1 or 2) tiles of 16
+// rows x 4 / kMT key groups; a warp walks its own pages with an online softmax of its own, kStages
 // steps of 8 KB in flight through shared memory by cp.async: a step's K rows are 4 KB in a row, and so are its
 // V rows.  The fragments of mma.sync come from there 16 bytes a lane, which works because the order of the
 // summed index of a product is free:
@@ -133,15 +133,13 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
   constexpr int kSteps = kPage / kKeys;           // steps of a page
   constexpr int kRowBytes = 128 * sizeof(E);
   constexpr int kKW = kWarps / kMT;   // key groups
-  constexpr int kR = 16 * kMT;        // query rows of the CTA
   extern __shared__ __align__(16) float sm[];   // the ring, then [kWarps][16][kRowFloats] partials
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, t = lane & 3;
   const int mt = warp / kKW, kw = warp - mt * kKW;
   const int split = blockIdx.x, g = blockIdx.y;
-  const int b = blockIdx.z / a.r_tiles, rt = blockIdx.z - b * a.r_tiles;
-  const int all = a.m * a.G;
-  const int rows = min(kR, all - rt * kR);   // live rows of the CTA
+  const int b = blockIdx.z;
+  const int rows = a.m * a.G;   // 16 kMT at most
 
   int len = 0;
   if constexpr (kShare != kPrefixPass) {
@@ -156,7 +154,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
     if constexpr (kShare == kPrefixPass) return a.key_end;
     return len + min((r / a.G) / a.block_size * a.block_size + a.block_size, a.m);
   };
-  const int kv_end = seen_by(rt * kR + rows - 1);   // the last row sees the most
+  const int kv_end = seen_by(rows - 1);   // the last row sees the most
   const int n_pages = (kv_end + kPage - 1) / kPage;
   const int per = (n_pages + a.S - 1) / a.S;
   const int pg_lo = split * per, pg_hi = min(n_pages, pg_lo + per);
@@ -202,8 +200,8 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
   if constexpr (kShare == kPrefixPass) pdl_launch_dependents();
 
   // Q fragments; for e4m3 scaled by 2^-e of each row's largest element
-  const int ra = rt * kR + mt * 16 + g8, rb = ra + 8;   // rows of the (sequence, kv head)
-  const int va = ra < all ? seen_by(ra) : 0, vb = rb < all ? seen_by(rb) : 0;
+  const int ra = mt * 16 + g8, rb = ra + 8;   // rows of the (sequence, kv head)
+  const int va = ra < rows ? seen_by(ra) : 0, vb = rb < rows ? seen_by(rb) : 0;
   uint32_t qf[8][4];
   float c_a = a.scale_log2, c_b = a.scale_log2;   // the scores' scale to log2 units
   {
@@ -218,7 +216,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
         const int r = h ? rb : ra;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint4 w = r < all ? *reinterpret_cast<const uint4*>(q_row(r) + c * 32 + t * 8) : make_uint4(0, 0, 0, 0);
+          const uint4 w = r < rows ? *reinterpret_cast<const uint4*>(q_row(r) + c * 32 + t * 8) : make_uint4(0, 0, 0, 0);
           qf[2 * c][h] = w.x;
           qf[2 * c][2 + h] = w.y;
           qf[2 * c + 1][h] = w.z;
@@ -233,7 +231,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-          if (r < all) {
+          if (r < rows) {
             w[0] = *reinterpret_cast<const uint4*>(q_row(r) + c * 64 + t * 16);
             w[1] = *reinterpret_cast<const uint4*>(q_row(r) + c * 64 + t * 16 + 8);
           }
@@ -436,10 +434,9 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
   float vs = 1.f;
   if constexpr (kQ8) vs = a.v_scale[g];
   if constexpr (kShare == kOwnPass) pdl_wait();   // the prefix pass has written its partials
-  auto store_row = [&](int r, float4 v, float M, float L) {   // dims 4 lane .. of row r of the CTA, merged
-    const int row = rt * kR + r;
-    const int pos = row / a.G;
-    const size_t at = (static_cast<size_t>(b) * a.m + pos) * a.Hq + static_cast<size_t>(g) * a.G + (row - pos * a.G);
+  auto store_row = [&](int r, float4 v, float M, float L) {   // dims 4 lane .. of row r, merged
+    const int pos = r / a.G;
+    const size_t at = (static_cast<size_t>(b) * a.m + pos) * a.Hq + static_cast<size_t>(g) * a.G + (r - pos * a.G);
     if constexpr (kShare == kPrefixPass) {
       reinterpret_cast<float4*>(a.part.o)[at * 32 + lane] = v;
       if (lane == 0) a.part.ml[at] = make_float2(M, L);
@@ -447,7 +444,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
     }
     if constexpr (kShare == kOwnPass)
       if (a.part.o != nullptr) {
-        if (a.part.per) share_add_runs(a.part, g, b * a.m * a.G + row, lane, M, L, v);
+        if (a.part.per) share_add_runs(a.part, g, b * rows + r, lane, M, L, v);
         else share_add(a.part.ml[at], reinterpret_cast<const float4*>(a.part.o)[at * 32 + lane], M, L, v);
       }
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at * 128;
@@ -528,13 +525,11 @@ __global__ void __launch_bounds__(32 * kWarps, 3) attn_small_kernel(const AttnSm
 
 }  // namespace
 
-// Query rows per CTA, row tiles and KV splits of a launch.
+// 16-row tiles and KV splits of a launch.
 void attn_small_plan(int batch, int max_len, int sms, AttnSmallArgs& a) {
-  const int rows = a.m * a.G;
-  a.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  a.r_tiles = (rows + 16 * a.mt - 1) / (16 * a.mt);
+  a.mt = a.m * a.G <= 16 ? 1 : 2;
   const int pages = (max_len + kPage - 1) / kPage;
-  const long long units = static_cast<long long>(batch) * a.r_tiles * a.Hkv;
+  const long long units = static_cast<long long>(batch) * a.Hkv;
   // splits until every SM holds its three CTAs twice, of a page per key group at least; once beside a prefix, where a
   // sequence's own keys are few (64 sequences of up to 512 keys under one of 16384: 63 -> 55 us for both passes)
   const int kw = kWarps / a.mt;
@@ -547,7 +542,7 @@ namespace {
 using SmallKernel = void (*)(const AttnSmallArgs);
 template <typename E, int kShare>
 SmallKernel small_kernel(int mt) {
-  return mt == 1 ? attn_small_kernel<1, E, kShare> : mt == 2 ? attn_small_kernel<2, E, kShare> : attn_small_kernel<4, E, kShare>;
+  return mt == 1 ? attn_small_kernel<1, E, kShare> : attn_small_kernel<kSmallRows / 16, E, kShare>;
 }
 SmallKernel small_kernel(int mt, int share) {
   if (share == kPrefixPass) return small_kernel<__nv_bfloat16, kPrefixPass>(mt);
@@ -563,13 +558,13 @@ cudaError_t launch_attention_small(cudaStream_t st, const AttnSmallArgs& a, int 
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
     for (int share : {0, kOwnPass, kPrefixPass})
-      for (int mt : {1, 2, 4})
+      for (int mt : {1, 2})
         if ((e = cudaFuncSetAttribute(small_kernel(mt, share), cudaFuncAttributeMaxDynamicSharedMemorySize, kRing)) != cudaSuccess)
           return e;
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.S, a.Hkv, batch * a.r_tiles);
+  cfg.gridDim = dim3(a.S, a.Hkv, batch);
   cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = kRing;
   cfg.stream = st;

@@ -2271,7 +2271,7 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
 // 34.8 at 16000, 64 rows 98 / 36.
 static bool small_tiles(long long rows, bool prefix, int keys) {
   if (prefix && keys > 2048) return rows <= 16;
-  return rows <= 32;
+  return rows <= kSmallRows;
 }
 
 // Argument checks common to the attention operators below.
@@ -2327,7 +2327,7 @@ nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float*
     AttnSmallArgs a{};
     fill(a);
     attn_small_plan(batch, max_len, sms, a);
-    if (static_cast<long long>(batch) * a.r_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
+    if (batch > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
     e = launch_attention_small(st, a, batch, false);
   } else {
     AttnWideArgs a{};
@@ -2403,7 +2403,7 @@ nld_status nld_attention_shared(const void* d_q, const void* d_kv_pool, const in
       AttnSmallArgs a{};
       fill(a);
       attn_small_plan(seqs, max_keys, sms, a);
-      if (static_cast<long long>(seqs) * a.r_tiles > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
+      if (seqs > 65535) return fail(nullptr, NLD_ERR_ARG, "batch*query tiles too large");
       if (launch) e = launch_attention_small(st, a, seqs, pdl);
     } else {
       AttnWideArgs a{};

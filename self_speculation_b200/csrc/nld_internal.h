@@ -190,8 +190,6 @@ struct QkvWriteArgs {
 // The two launches of the shared-prefix attention (`share` below; 0: nld_attention_q8).
 constexpr int kOwnPass = 1, kPrefixPass = 2;
 
-// Attention for small query tiles: over the e4m3 cache (nld_attention_q8), or a pass of the
-// shared-prefix attention over the bf16 cache.
 // Where the prefix pass leaves its rows' unnormalised (O, max, sum), and where the own pass finds them.  per == 0: a row's
 // place is token x Hq + head.  Otherwise the pass was cut into CTAs of `per` pages along all of its (kv head, query tile,
 // page), so that CTA c's part of tile u is 128 rows at place u + c (either grows with every part).
@@ -202,6 +200,10 @@ struct ShareParts {
 };
 constexpr int kShareCtas = 160; // CTAs of such a pass at most
 
+// Attention for small query tiles: over the e4m3 cache (nld_attention_q8), or a pass of the
+// shared-prefix attention over the bf16 cache.
+constexpr int kSmallRows = 32;  // rows of a kv head, positions x heads, at most
+
 struct AttnSmallArgs {
   const void* q;                // [batch, m, Hq, 128] bf16
   void* out;
@@ -211,7 +213,7 @@ struct AttnSmallArgs {
   const int* page_table;
   int pps, n_pages;
   int m, Hq, Hkv, G, block_size;
-  int mt, r_tiles, S;           // 16-row tiles of a CTA, tiles of query rows, KV splits (cluster size)
+  int mt, S;                    // 16-row tiles, KV splits (cluster size)
   float scale_log2;             // log2(e) / sqrt(hd)
   int share;                    // 0: e4m3; kOwnPass or kPrefixPass: bf16
   int key_end;                  // prefix pass: keys of the prefix
