@@ -459,7 +459,8 @@ nld_status nld_attention(const void* d_q, const void* d_kv_pool, const int32_t* 
  *                    p * theta^(-2j/hd), j = 0..hd/2-1.
  *   position_offset  position of cache slot 0 (the length of a shared prefix; else 0).
  *   d_rows           [batch] or NULL: the first rows[b] of the m rows of sequence b are live, the
- *                    others are padding: nothing of them is read or written.
+ *                    others are padding: nothing of them is read or written.  (Attention over such a
+ *                    batch: see nld_attention_q8.)
  *   d_q_out          [batch, m, Hq, hd] of `dtype`; may be d_q where q_ld = Hq*hd.
  *   d_kv_pool        [n_pages][2][Hkv][64][hd] of `kv_dtype` (K then V per page).  NLD_F32 and
  *                    NLD_BF16 rows are rounded once from fp32; NLD_E4M3 rows are e4m3(x / scale),
@@ -490,6 +491,11 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
  *   d_err        one int32 or NULL: a lens[b] outside 0..pages_per_seq*64-m is clamped, a page id
  *                outside the pool reads as zeros, and NLD_DEVERR_KV_OVERFLOW is or-ed in;
  *                NLD_DEVERR_TIMEOUT if a bounded wait ran out.
+ * Padded batches (d_rows of nld_qk_norm_rope): every sequence has m queries here, so the slots of its
+ * padding rows are keys that its padding queries see.  They must hold finite numbers (zero-fill the pool
+ * once) in pages that the table names (one page of zeros may stand for all of them: nothing writes there),
+ * and lens[b] + m slots must fit the table.  A live row sees the padding slots of its own block: give block_size
+ * 1, or multiples of block_size live rows.  The padding rows of d_q must be readable; those of d_out are written.
  * The other arguments, the mask and the conventions are those of nld_attention (d_q and d_out
  * bf16, 16-byte aligned).  Scores, maxima and sums are fp32; the probabilities are rounded to fp16's 11 bits for
  * their product with V (below 2^-25 of the row's largest to steps of 2^-35 of it).  Elements of a query row below 2^-9 of its largest may be off by 2^-17 of that
@@ -515,7 +521,8 @@ nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float*
  *   d_err           one int32 or NULL: a lens[b] outside 0..pages_per_seq*64-m is clamped, a page id
  *                   outside the pool reads as zeros, and NLD_DEVERR_KV_OVERFLOW is or-ed in;
  *                   NLD_DEVERR_TIMEOUT if a bounded wait ran out.
- * Slots behind a sequence's last key, and behind the prefix's, may hold anything.  Scores, maxima and sums
+ * Slots behind a sequence's last key, and behind the prefix's, may hold anything.  Padded batches are as in
+ * nld_attention_q8.  Scores, maxima and sums
  * are fp32; the probabilities are rounded to bf16 for their product with V.
  * Two launches on `cuda_stream` (one with shared_len 0); returns after them.
  */

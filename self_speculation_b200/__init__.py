@@ -381,7 +381,8 @@ def nld_attention_q8(q, kv_pool, k_scale, v_scale, page_table, lens, block_size:
                      stream: Optional[int] = None) -> None:
     """nld_attention over an e4m3 cache: kv_pool [n_pages, 2, Hkv, 64, 128] float8_e4m3fn, k_scale
     and v_scale [Hkv] fp32; q [B, m, Hq, 128] bf16, page_table [B, pps] int32, lens [B] int32, out
-    like q, err [1] int32 device error word."""
+    like q, err [1] int32 device error word.  A batch with padding rows (nld_qk_norm_rope's rows): their
+    slots must hold finite numbers, and block_size must divide the live rows (include/nld.h)."""
     _done(_native().attention_q8(q, kv_pool, k_scale, v_scale, page_table, lens, block_size, max_len, out, err, stream))
 
 
@@ -393,7 +394,8 @@ def nld_attention_shared(q, kv_pool, shared_pages, shared_len: int, page_table, 
                          workspace, err=None, stream: Optional[int] = None) -> None:
     """nld_attention for sequences that all start with the same shared_len keys, in the pages
     shared_pages [n] int32; page_table, lens and max_len count a sequence's own keys.  workspace: uint8
-    of nld_attention_shared_workspace_size bytes (None with shared_len 0)."""
+    of nld_attention_shared_workspace_size bytes (None with shared_len 0).  Padding rows as in
+    nld_attention_q8."""
     _done(_native().attention_shared(q, kv_pool, shared_pages, shared_len, page_table, lens, block_size, max_len, out,
                                      workspace, err, stream))
 
