@@ -6,6 +6,7 @@ Sources: self_speculation_b200/csrc/*.cu, public header include/nld.h.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -42,16 +43,28 @@ def _run(cmd, what: str, verbose: bool) -> subprocess.CompletedProcess:
     return r
 
 
+def operators_built_for() -> str:
+    """The Python and torch whose binary interfaces `_operators.so` is built against; the file holds this text."""
+    return f"built for {sysconfig.get_config_var('SOABI')}, torch {importlib.metadata.version('torch')};"
+
+
+def _operators_stale(target: str, deps) -> bool:
+    if _stale(target, deps):
+        return True
+    with open(target, "rb") as f:
+        return operators_built_for().encode() not in f.read()
+
+
 def _build_operators(force: bool, verbose: bool) -> None:
     source = os.path.join(CSRC, "bind_operators.cpp")
-    if not force and not _stale(OPERATORS, [source, os.path.join(ROOT, "include", "nld.h")]):
+    if not force and not _operators_stale(OPERATORS, [source, os.path.join(ROOT, "include", "nld.h")]):
         return
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     paths = [os.path.join(ROOT, "include"), *include_paths(), os.path.join(cuda, "include"), sysconfig.get_path("include")]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", source, "-o", OPERATORS + ".tmp"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DNLD_BUILT_FOR="{operators_built_for()}"', source, "-o", OPERATORS + ".tmp"]
     for p in paths:
         cmd += ["-isystem" if p != paths[0] else "-I", p]
     cmd += [f"-L{p}" for p in library_paths()]
