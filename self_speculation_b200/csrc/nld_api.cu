@@ -2265,10 +2265,15 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
 }
 
 // The kernel for small query tiles (mma.sync: its time grows with the rows of a kv head, positions x heads) or the one for
-// wide ones (tcgen05: a page costs the same for 1 row or 128, a launch 4 us more)?  Measured, small against wide,
-// 32 query and 8 kv heads: e4m3, 32 rows, 64 sequences of 2000 keys 101 / 125 us, 8 of 16000 117 / 102, 48 rows 68 / 36;
-// a shared prefix, 16 rows 15.3 / 17.0 us at 4000 keys and 35.3 / 34.5 at 16000, 32 rows 16.7 / 16.8 at 2000 and 56.8 /
-// 34.8 at 16000, 64 rows 98 / 36.
+// wide ones (tcgen05: a page costs the same for 1 row or 128)?  Measured, small against wide, us of a call after others'
+// data, 32 query and 8 kv heads.  e4m3, sequences x keys:
+//             1 x 500   1 x 16000   8 x 500   8 x 2000   8 x 16000   64 x 500   64 x 2000   64 x 8000
+//   4 rows    12 / 14   27 / 37     14 / 16   27 / 27     84 /  98   39 / 51     76 / 113   198 / 345
+//   16 rows   14 / 16   29 / 37     16 / 16   31 / 27     88 / 100   47 / 51     82 / 115   207 / 346
+//   32 rows   14 / 16   45 / 37     18 / 17   36 / 27    121 / 100   55 / 53    104 / 115   305 / 344
+// 17 to 32 rows are on the side of many sequences, whose steps take longest; few long ones lose up to 30 % by it.
+// A prefix (its pass alone is one sequence: the own pass beside it): 16 rows 17 / 21 us at 2000 keys, 21.5 / 23.6 at 4000, 40 /
+// 40 at 16000; 32 rows 17.4 / 19.5 at 1000, 21.4 / 21.5 at 2000, 26 / 23.6 at 4000, 60 / 40 at 16000.
 static bool small_tiles(long long rows, bool prefix, int keys) {
   if (prefix && keys > 2048) return rows <= 16;
   return rows <= kSmallRows;
