@@ -491,6 +491,8 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
  *   d_err        one int32 or NULL: a lens[b] outside 0..pages_per_seq*64-m is clamped, a page id
  *                outside the pool reads as zeros, and NLD_DEVERR_KV_OVERFLOW is or-ed in;
  *                NLD_DEVERR_TIMEOUT if a bounded wait ran out.
+ * NaN and infinities come out in the rows that see them; those in a V row may come out as NaN in earlier rows of
+ * the same sequence too, whose weight 0 multiplies them.
  * Padded batches (d_rows of nld_qk_norm_rope): every sequence has m queries here, so the slots of its
  * padding rows are keys that its padding queries see.  They must hold finite numbers (zero-fill the pool
  * once) in pages that the table names (one page of zeros may stand for all of them: nothing writes there),
