@@ -15,8 +15,8 @@
 // core), and 512 more if Q had to be read for every S.  The streams' partials meet in shared memory at the end,
 // those of the KV splits over the cluster's distributed shared memory, in a fixed order.
 //
-// What it measured (8 sequences of 16416 keys, 32 rows, 32 / 8 heads, e4m3: 88 us, 0.78 PFLOP/s; back to back
-// for longer the power limit takes the clock to 1.7 GHz, and that 102): two pages of 128 rows take
+// What it measured (8 sequences of 16416 keys, 32 rows, 32 / 8 heads, e4m3: 98 to 104 us, 0.68 PFLOP/s, at the 1.7 GHz that the
+// power limit leaves; 90 for the first 30 ms): two pages of 128 rows take
 // 1850 cycles, 55 % of the exponential unit; the rest is the latency of a softmax thread's steps (scores in 85 cycles,
 // maximum 175, exponentials 512 to 800, waits 370, P out 100).  Two threads a row (sixteen softmax warps) took 10 to
 // 17 % longer, a quarter of the exponentials as polynomials on the multiply-add pipe 1 to 6 %, the next page's scores
@@ -27,7 +27,7 @@
 // A prefix pass may have more query tiles than SMs, and then a round of clusters that few of them fill.  Where it costs less,
 // it is cut into runs of pages (kRuns): a CTA an SM takes as many pages as any other, across query tiles.  Each tile's part
 // goes to the workspace as it lies in shared memory, by a copy beside which the next part starts, and the own pass adds
-// the parts of a row in their order.  16 sequences x 32 rows of 40 / 8 heads over 4133 shared and 300 own keys: 97 -> 82 us;
+// the parts of a row in their order.  16 sequences x 32 rows of 40 / 8 heads over 4133 shared and 300 own keys: 97 us in clusters, 84 so;
 // 20 x 32 rows of 32 / 8 heads over 6000: 120 -> 100; 64 rows a kv head over 16384, in clusters: 47.
 //
 // bf16: K and V come by TMA into rings of six pages.  e4m3: K's page goes to the tensor core as it comes (kind::f8f6f4)
