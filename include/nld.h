@@ -499,9 +499,10 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
  * and lens[b] + m slots must fit the table.  A live row sees the padding slots of its own block: give block_size
  * 1, or multiples of block_size live rows.  The padding rows of d_q must be readable; those of d_out are written.
  * The other arguments, the mask and the conventions are those of nld_attention (d_q and d_out
- * bf16, 16-byte aligned).  Scores, maxima and sums are fp32; the probabilities are rounded to fp16's 11 bits for
- * their product with V (below 2^-25 of the row's largest to steps of 2^-35 of it).  Elements of a query row below 2^-9 of its largest may be off by 2^-17 of that
- * one in its products with K (below 2^-14 of it by 2^-25, for the small tiles).
+ * bf16, 16-byte aligned).  Scores, maxima and sums are fp32; the probabilities are rounded to fp16's 11
+ * bits for their product with V (below 2^-25 of the row's largest to steps of 2^-35 of it).  Elements of a
+ * query row below 2^-9 of its largest may be off by 2^-17 of that one in its products with K (below 2^-14 of
+ * it by 2^-25, for the small tiles).
  */
 nld_status nld_attention_q8(const void* d_q, const void* d_kv_pool, const float* d_k_scale, const float* d_v_scale,
                             const int32_t* d_page_table, int pages_per_seq, int n_pages, const int32_t* d_lens,

@@ -2272,7 +2272,7 @@ nld_status nld_qk_norm_rope(const void* d_q, long long q_ld, const void* d_k, lo
 //   16 rows   14 / 16   29 / 37     16 / 16   31 / 27     88 / 100   47 / 51     82 / 115   207 / 346
 //   32 rows   14 / 16   45 / 37     18 / 17   36 / 27    121 / 100   55 / 53    104 / 115   305 / 344
 // 17 to 32 rows are on the side of many sequences, whose steps take longest; few long ones lose up to 30 % by it.
-// A prefix (its pass alone is one sequence: the own pass beside it): 16 rows 17 / 21 us at 2000 keys, 21.5 / 23.6 at 4000, 40 /
+// A prefix, with its batch's rows together (both passes, few own keys): 16 rows 17 / 21 us at 2000 keys, 21.5 / 23.6 at 4000, 40 /
 // 40 at 16000; 32 rows 17.4 / 19.5 at 1000, 21.4 / 21.5 at 2000, 26 / 23.6 at 4000, 60 / 40 at 16000.
 static bool small_tiles(long long rows, bool prefix, int keys) {
   if (prefix && keys > 2048) return rows <= 16;
